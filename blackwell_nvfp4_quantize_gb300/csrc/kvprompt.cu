@@ -25,6 +25,13 @@
 //   warp 12    of the first CTA issues tcgen05.mma (kind::f16): S = Q K^T from
 //              shared memory, O += P V with P as fp16 in TMEM, over the columns
 //              S came in.
+//   warps 13, 14 of the second CTA pass on to it that operands and queries are
+//              in place there: what one CTA wrote to its shared memory for an MMA
+//              of the other needs a release at cluster scope, which costs the warp
+//              about 1300 cycles, and these have the time.
+// K and V of a block are handed over together: the hand-offs (a proxy fence and a
+// release, which wait for the loads on their way) are what the operands' warps
+// have least time for (prompt_chunk 955 us, with one for each 1000).
 // S, P and the products go page by page (64 tokens): a warpgroup alternates
 // between its tile's two pages, and while it works on one the tensor core takes
 // the other's P, refills its S, and serves the other tile.  TMEM: S 2 x 128 columns, O 2 x D.
@@ -52,6 +59,7 @@ namespace {
 
 constexpr int kRowsPair = 512;
 constexpr int kStages = 4;  // of K and V
+constexpr int kSeen = 8;    // blocks whose pages the rows' warps may still ask about
 constexpr int kBlockKeys = 128;
 constexpr int kWarpDq = 8, kWarpMma = 12;
 // Four warpgroups: two for the rows, one for the operands, one whose first
@@ -73,7 +81,7 @@ struct PromptSmem {
   static constexpr int kK = kQ + 2 * kQTile;
   static constexpr int kV = kK + kStages * kKTile;
   static constexpr int kBars = kV + kStages * kVTile;
-  static constexpr int kNumBars = 2 + 4 * kStages + 4 + 4 + 4 + 1;
+  static constexpr int kNumBars = 2 + 3 * kStages + 4 + 4 + 4 + 1 + 2 + kStages + kSeen;
   static constexpr int kMisc = kBars + kNumBars * 8;
   static constexpr int kPrefix = kMisc + 128;
   static int bytes(int B) {
@@ -191,14 +199,53 @@ __device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 // One lane arrives on a barrier of the first CTA (its address there: bar), from
-// either CTA.  What the MMAs will read has been completed before by the fences
-// of its kind (tcgen05.wait::st, fence.proxy.async); an arrival that releases at
-// cluster scope costs 1300 cycles here (measured).
-__device__ __forceinline__ void arrive_first(uint32_t bar) {
+// either CTA: the warp's P is in TMEM.  Between tcgen05 operations of different
+// threads it is the tcgen05 fences (before this, and after the wait) that order,
+// and the barrier has to say no more than that it was reached.
+__device__ __forceinline__ void arrive_tmem(uint32_t bar) {
   asm volatile(
       "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
       "@e mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n}\n" ::"r"(bar)
       : "memory");
+}
+// One lane arrives on a barrier of its own CTA: what the warp wrote to shared
+// memory before, and fenced for the MMAs' proxy, is in place there.
+__device__ __forceinline__ void arrive_smem(uint32_t bar) {
+  __syncwarp();
+  asm volatile(
+      "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+      "@e mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar)
+      : "memory");
+}
+// One lane passes on to a barrier of the first CTA what its warp has acquired from a barrier of its own.
+__device__ __forceinline__ void arrive_onward(uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+      "@e mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n}\n" ::"r"(bar)
+      : "memory");
+}
+// The issuing warp's waits, on arrivals from both CTAs: with the operands' writes
+// (SMEM), or for tcgen05 operations alone.
+template <bool SMEM>
+__device__ __forceinline__ bool pair_try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  if constexpr (SMEM)
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  return ok != 0;
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -219,21 +266,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
   using L_ = PromptSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  // the first CTA's: arrivals from the warps of both
+  // the first CTA's: arrivals of its own warps and, from the other CTA, of the warp that passes them on
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L_::kBars);  // [2] tiles, per segment
-  uint64_t* k_full = q_full + 2;                                    // [kStages]
-  uint64_t* v_full = k_full + kStages;
-  uint64_t* p_full = v_full + kStages;  // [2 tiles][2 pages]
+  uint64_t* kv_full = q_full + 2;                                   // [kStages]
+  uint64_t* p_full = kv_full + kStages;  // [2 tiles][2 pages]; of the warps of both
   // each CTA's own: commits
   uint64_t* k_empty = p_full + 4;
   uint64_t* v_empty = k_empty + kStages;
   uint64_t* s_full = v_empty + kStages;  // [2 tiles][2 pages]
   uint64_t* o_full = s_full + 4;         // [2 tiles][2 pages]
   uint64_t* drain = o_full + 4;
+  // the second CTA's: arrivals of its own warps
+  uint64_t* q_mine = drain + 1;
+  uint64_t* kv_mine = q_mine + 2;
+  // each CTA's own: seen[k % kSeen] is written
+  uint64_t* seen_full = kv_mine + kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L_::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L_::kMisc + 4);
-  // whether the pages of block k count, at [k % 8][page]: block k + 8 is staged only after every row is done with k
-  volatile uint8_t* seen = smem + L_::kMisc + 8;
+  // whether the pages of block k count, a bit each, at [k % kSeen]: block k + 8 is staged only after every row is done with k
+  uint8_t* seen = smem + L_::kMisc + 8;
   int* scratch = reinterpret_cast<int*>(smem + L_::kMisc + 32);  // 16 ints
   int* prefix = reinterpret_cast<int*>(smem + L_::kPrefix);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -242,19 +293,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
   const uint32_t first_bars = cluster_map(smem_u32(q_full), 0);  // the first CTA's barriers, in the order above
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + i, 8);  // one arrival per warp, four in each CTA
+      mbar_init(q_full + i, 5);  // four warps and the one that passes on
+      mbar_init(q_mine + i, 4);
       for (int h = 0; h < 2; ++h) {
-        mbar_init(p_full + 2 * i + h, 8);
+        mbar_init(p_full + 2 * i + h, 8);  // one arrival per warp, four in each CTA
         mbar_init(s_full + 2 * i + h, 1);
         mbar_init(o_full + 2 * i + h, 1);
       }
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(k_full + i, 8);
-      mbar_init(v_full + i, 8);
+      mbar_init(kv_full + i, 5);
+      mbar_init(kv_mine + i, 4);
       mbar_init(k_empty + i, 1);
       mbar_init(v_empty + i, 1);
     }
+    for (int i = 0; i < kSeen; ++i) mbar_init(seen_full + i, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -334,8 +387,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
         *reinterpret_cast<uint4*>(qs + (i >> 3) * (128 * 128) + swz(row, i & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
       }
       fence_proxy_async_smem();
-      __syncwarp();
-      arrive_first(first_bars + 8 * t);
+      arrive_smem(smem_u32((rank == 0 ? q_full : q_mine) + t));
       return pow2i(e - 140);
     };
     float down = 1.0f;
@@ -392,17 +444,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
       // the warp's rows: the first and the last slot they sit at
       const int at_lo = __reduce_min_sync(0xFFFFFFFFu, at), at_hi = __reduce_max_sync(0xFFFFFFFFu, at);
       float m = -INFINITY, l = 0.0f;
+      uint32_t pages = 3u;  // of the block at hand: bit i, page i counts
       // page by page: while this warpgroup works on one page's scores, the tensor
       // core takes the other's P and refills its S
       for (int i = 0; i < 2 * nblk; ++i) {
         const int pg = i & 1;
+        if (pg == 0) {  // (long there when the scores come, and here it costs nothing)
+          ok = mbar_wait(seen_full + ks % kSeen, ks / kSeen & 1, abort_flag, p.g.status, 83);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          pages = seen[ks % kSeen];
+        }
         ok = mbar_wait(s_full + 2 * t + pg, kc & 1, abort_flag, p.g.status, 72);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint32_t tp = ts + kPage * pg;
         const int slot0 = (x.first + (u + (i >> 1) - x.begin)) * kBlockKeys + kPage * pg;
-        const bool there = seen[2 * (ks & 7) + pg] != 0;
+        const bool there = (pages >> pg) & 1u;
         // tokens lo < k <= hi of the page are seen
         const int hi = at - slot0, lo = p.window > 0 ? hi - p.window : -1;
         const bool masked = slot0 + kPage - 1 > at_lo || (p.window > 0 && slot0 <= at_hi - p.window) || !there;
@@ -483,7 +542,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        arrive_first(first_bars + 8 * (2 + 2 * kStages + 2 * t + pg));
+        arrive_tmem(first_bars + 8 * (2 + kStages + 2 * t + pg));
         kc += pg;
         ks += pg;
       }
@@ -632,7 +691,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
       }
-      if (w == 0 && lane < 2) seen[2 * (k & 7) + lane] = (seen_of(cur) >> lane) & 1u;
+      if (w == 0 && lane == 0) {
+        seen[k % kSeen] = static_cast<uint8_t>(seen_of(cur));
+        mbar_arrive(seen_full + k % kSeen);
+      }
       uint8_t* kt = smem + L_::kK + s * L_::kKTile;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -665,9 +727,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
           *reinterpret_cast<uint4*>(kt + (unit >> 3) * (kPage * 128) + swz(r, unit & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
         }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      arrive_first(first_bars + 8 * (2 + s));
       if (k >= kStages) {
         ok = mbar_wait(v_empty + s, (k / kStages - 1) & 1, abort_flag, p.g.status, 76);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -699,8 +758,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
         }
       }
       fence_proxy_async_smem();
-      __syncwarp();
-      arrive_first(first_bars + 8 * (2 + kStages + s));
+      arrive_smem(smem_u32((rank == 0 ? kv_full : kv_mine) + s));
       load_k(bytes_of(next, pv));
       load_v(bytes_of(next, pv));
       cur = next;
@@ -714,18 +772,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
         int k = 0, nk[2] = {0, 0}, ns[2] = {0, 0};  // blocks of the pair; blocks and segments of each tile
         bool ok = true;
         constexpr uint32_t kBarBase = kSmemBase + L_::kBars;  // the barriers in the order above
-        constexpr uint32_t bKEmpty = kBarBase + 8 * (2 + 2 * kStages + 4), bVEmpty = bKEmpty + 8 * kStages;
+        constexpr uint32_t bKEmpty = kBarBase + 8 * (2 + kStages + 4), bVEmpty = bKEmpty + 8 * kStages;
         constexpr uint32_t bS = bVEmpty + 8 * kStages, bO = bS + 8 * 4, bDrain = bO + 8 * 4;
-        auto wait = [&](uint64_t* bar, int phase, unsigned site) {
-          ok = ok && mbar_wait(bar, phase & 1, abort_flag, p.g.status, site);
+        auto wait_for = [&](auto smem_too, uint64_t* bar, int phase, unsigned site) {
+          ok = ok && bounded_wait([&]() { return pair_try_wait<smem_too.value>(bar, phase & 1); }, abort_flag, p.g.status, site);
           ok = __all_sync(0xFFFFFFFFu, ok);
           tc_fence_after();
         };
+        auto wait = [&](uint64_t* bar, int phase, unsigned site) { wait_for(std::true_type{}, bar, phase, site); };
+        auto wait_p = [&](uint64_t* bar, int phase) { wait_for(std::false_type{}, bar, phase, 79); };
         for (int u = start; u < end && ok;) {
           const Unit x = find_unit<kRowsPair, kBlockKeys>(p, prefix, u);
           const int seg_end = min(end, x.end), nblk = seg_end - u;
           const bool two = x.r0 + 256 <= x.r1;
-          wait(k_full + k % kStages, k / kStages, 77);
+          wait(kv_full + k % kStages, k / kStages, 77);
           wait(q_full, ns[0]++, 78);
           if (two) wait(q_full + 1, ns[1]++, 78);
           if (!ok) break;
@@ -738,29 +798,28 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
           });
           for (int j = 0; j < nblk && ok; ++j, ++k, ++nk[0], nk[1] += two) {
             const bool more = j + 1 < nblk;
-            wait(v_full + k % kStages, k / kStages, 80);
-            if (more) wait(k_full + (k + 1) % kStages, (k + 1) / kStages, 81);
+            if (more) wait(kv_full + (k + 1) % kStages, (k + 1) / kStages, 80);
             if (!ok) break;
             by_stage(k % kStages, [&](auto s) {
               constexpr int S = s.value, S1 = (S + 1) % kStages;
               // page 0 of the tiles, then page 1: P in, the page's S of the next block out
-              wait(p_full, nk[0], 79);
+              wait_p(p_full, nk[0]);
               if (!ok) return;
               issue_pv<D, 0, 0, S>(bO, j > 0);
               if (more) issue_qk<D, 0, 0, S1>(bS);
               if (two) {
-                wait(p_full + 2, nk[1], 79);
+                wait_p(p_full + 2, nk[1]);
                 if (!ok) return;
                 issue_pv<D, 1, 0, S>(bO, j > 0);
                 if (more) issue_qk<D, 1, 0, S1>(bS);
               }
-              wait(p_full + 1, nk[0], 79);
+              wait_p(p_full + 1, nk[0]);
               if (!ok) return;
               issue_pv<D, 0, 1, S>(bO, true);
               if (!two) tc_commit2(bVEmpty + 8 * S);
               if (more) issue_qk<D, 0, 1, S1>(bS);
               if (two) {
-                wait(p_full + 3, nk[1], 79);
+                wait_p(p_full + 3, nk[1]);
                 if (!ok) return;
                 issue_pv<D, 1, 1, S>(bO, true);
                 tc_commit2(bVEmpty + 8 * S);
@@ -773,7 +832,26 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
         }
         tc_commit2(bDrain);
       }
-    } else if (warp == kWarpMma + 1 && rank == 0) {
+    } else if (rank == 1) {
+      // ------------------------------------------------------ passing on
+      auto pass = [&](uint64_t* bar, int phase, uint32_t to) {
+        const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase & 1, abort_flag, p.g.status, 81));
+        if (ok) arrive_onward(to);
+        return ok;
+      };
+      if (warp == kWarpMma + 1) {
+        for (int k = 0; k < end - start; ++k)
+          if (!pass(kv_mine + k % kStages, k / kStages, first_bars + 8 * (2 + k % kStages))) break;
+      } else if (warp == kWarpMma + 2) {
+        int ns[2] = {0, 0};  // in the order in which they are waited for
+        for (int u = start; u < end;) {
+          const Unit x = find_unit<kRowsPair, kBlockKeys>(p, prefix, u);
+          if (!pass(q_mine, ns[0]++, first_bars)) break;
+          if (x.r0 + 256 <= x.r1 && !pass(q_mine + 1, ns[1]++, first_bars + 8)) break;
+          u = min(end, x.end);
+        }
+      }
+    } else if (warp == kWarpMma + 1) {
       // for the join: the problem that begins in this run and does not end in it
       const Unit x = find_unit<kRowsPair, kBlockKeys>(p, prefix, end - 1);
       const bool split = x.begin >= start && x.end > end;

@@ -54,16 +54,16 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Bounded wait on a phase parity.  Gives up when *abort becomes nonzero (some
-// other role gave up) or after limit_ns (FP4ATTN_WAIT_NS unless a test asks
+// Bounded wait: try_wait() until it holds.  Gives up when *abort becomes nonzero
+// (some other role gave up) or after limit_ns (FP4ATTN_WAIT_NS unless a test asks
 // for less); in the latter case records the failure and raises *abort.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                          DeviceStatus* status, unsigned site,
-                                          uint64_t limit_ns = FP4ATTN_WAIT_NS) {
-  if (mbar_try_wait(bar, parity)) return true;
+template <typename Try>
+__device__ __forceinline__ bool bounded_wait(Try&& try_wait, volatile int* abort, DeviceStatus* status, unsigned site,
+                                             uint64_t limit_ns = FP4ATTN_WAIT_NS) {
+  if (try_wait()) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (try_wait()) return true;
     if (*abort) return false;
     if (globaltimer_ns() - t0 > limit_ns) {
       *abort = 1;
@@ -73,6 +73,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
       return false;
     }
   }
+}
+
+// The same on a phase parity.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          DeviceStatus* status, unsigned site,
+                                          uint64_t limit_ns = FP4ATTN_WAIT_NS) {
+  return bounded_wait([&]() { return mbar_try_wait(bar, parity); }, abort, status, site, limit_ns);
 }
 
 // Wait for asynchronous work this CTA has already issued (TMA copies into its
