@@ -122,11 +122,11 @@ __device__ __forceinline__ void load_columns(const KvAttnParams& p, const Unit& 
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
       q.q[nt][i] = pack_half2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
-    const float cs = MOD && p.cap > 0.0f ? p.scale / p.cap : p.scale * kLog2Ef;
+    const float cs = score_factor<MOD>(p, down);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int col = x.r0 + nt * 8 + 2 * c + k;
-      q.cs[nt][k] = cs * __shfl_sync(0xFFFFFFFFu, down, (2 * c + k) * 4);
+      q.cs[nt][k] = __shfl_sync(0xFFFFFFFFu, cs, (2 * c + k) * 4);
       q.at[nt][k] = col <= x.r1 ? x.L - x.n + col / p.G : kNoColumn;
       q.slope[nt][k] = 0.0f;
       if (MOD && p.slopes && col <= x.r1) q.slope[nt][k] = p.slopes[x.h * p.G + col % p.G] * kLog2Ef;
@@ -1041,9 +1041,9 @@ int check_attn(const fp4attn_kv_cache_t* c, const fp4attn_kv_batch_t* b, const v
   if (st != FP4ATTN_OK) return st;
   if (group <= 0 || max_new < 0 || max_new > b->T || window < 0) return FP4ATTN_ERR_INVALID_ARG;
   if (!b->cu && max_new != b->T / b->B) return FP4ATTN_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || scale <= 0.0f || !std::isfinite(cap) || cap < 0.0f) return FP4ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || scale <= 0.0f || !(cap >= 0.0f && cap <= kMaxCap)) return FP4ATTN_ERR_INVALID_ARG;
   const float up = scale * ldexpf(1.0f, c->k_exp);  // what the kernels multiply by
-  if (!std::isfinite(up) || up == 0.0f || (cap > 0.0f && !std::isfinite(up / cap))) return FP4ATTN_ERR_INVALID_ARG;
+  if (!std::isnormal(up) || (cap > 0.0f && !std::isfinite(up / cap))) return FP4ATTN_ERR_INVALID_ARG;
   if (b->T > 0 && (!q || !aligned16(q) || ((q_row | q_head) & 7))) return FP4ATTN_ERR_INVALID_ARG;
   if (static_cast<long long>(c->heads) * group > 65535) return FP4ATTN_ERR_UNSUPPORTED;
   // units of all tiles must stay within 32 bits

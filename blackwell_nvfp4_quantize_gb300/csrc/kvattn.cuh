@@ -1,6 +1,7 @@
 // Shared by the attention kernels over the 4-bit key/value cache: arguments,
 // the even split of the work, and how partial results are joined.
 #pragma once
+#include <cfloat>
 #include <cmath>
 
 #include "kvcache.cuh"
@@ -8,6 +9,7 @@
 namespace fp4attn {
 
 constexpr int kNoColumn = -(1 << 30);  // below every slot, and slots stay below 2^30
+constexpr float kMaxCap = 1.2379400392853803e27f;  // 2^90: see score_factor
 constexpr int kMaxWindow = 1 << 30;       // no sequence is longer; slots minus windows stay within 32 bits
 constexpr float kLog2Ef = 1.4426950408889634f;
 constexpr float kLn2f = 0.6931471805599453f;
@@ -143,6 +145,18 @@ __device__ __forceinline__ Unit find_unit(const KvAttnParams& p, const int* pref
 }
 
 __device__ __forceinline__ int run_length(int units, int ctas) { return max(1, (units + ctas - 1) / ctas); }
+
+// What turns a row's S into its log2-domain scores (with a cap: into s / cap),
+// where its elements were multiplied by 1 / down, a power of two.  Masked scores
+// are -inf when this multiplies them, so it is never 0 there: S is below 2^34,
+// and what the least normal number makes of that is as good as 0.  (With a cap
+// or slopes the mask comes later, and a subnormal factor is off by 2^-150: below
+// 2^-24 of a score's unit for every cap that is accepted.)
+template <bool MOD>
+__device__ __forceinline__ float score_factor(const KvAttnParams& p, float down) {
+  const float f = p.scale * down;
+  return MOD ? fminf(p.cap > 0.0f ? f / p.cap : f * kLog2Ef, FLT_MAX) : fminf(fmaxf(f * kLog2Ef, FLT_MIN), FLT_MAX);
+}
 
 // Floats of one partial result: O [cols][D], max [cols], sum [cols].
 template <int D>

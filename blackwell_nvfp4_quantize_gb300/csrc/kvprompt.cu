@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
       const bool real = x.r0 + col <= x.r1;
       const int r = min(x.r1, x.r0 + col), at = x.L - x.n + r / p.G;
       // log2-domain score per unit of S (with a cap: s / cap)
-      const float cs = (MOD && p.cap > 0.0f ? p.scale / p.cap : p.scale * kLog2Ef) * down;
+      const float cs = score_factor<MOD>(p, down);
       const float slope = MOD && p.slopes ? p.slopes[x.h * p.G + r % p.G] * kLog2Ef : 0.0f;
       const float cap = p.cap * kLog2Ef;
       // S (in TMEM at tp, and in v) -> log2-domain scores; dist: of the first one

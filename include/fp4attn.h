@@ -494,11 +494,12 @@ int fp4attn_kv_attention_workspace_bytes(int heads, int D, int B, int max_pages,
  * first).  q: bf16 [T, heads * group, D] at the given strides in elements;
  * query head h uses KV head h / group.  Query i of a sequence with n new tokens
  * sits at slot lens - n + i and sees the slots j <= its own and, with window >
- * 0, with j > its own - window.  Scores s = softmax_scale q.k; softcap c > 0: s
- * = c tanh(s / c); slopes (fp32 [heads * group], may be NULL): s -= slope * (own
- * slot - j).  o: bf16 [T, heads * group, D] = softmax(s) V; lse: fp32 [T, heads *
- * group], natural log.  A query that sees nothing (a negative slot) gets o = 0,
- * lse = -inf.  max_new: no sequence has more new tokens (cu NULL: T / B).
+ * 0, with j > its own - window.  Scores s = softmax_scale q.k (softmax_scale
+ * 2^k_exp has to be a normal number); softcap c > 0, up to 2^90: s = c tanh(s /
+ * c); slopes (fp32 [heads * group], may be NULL): s -= slope * (own slot - j).
+ * o: bf16 [T, heads * group, D] = softmax(s) V; lse: fp32 [T, heads * group],
+ * natural log.  A query that sees nothing (a negative slot) gets o = 0, lse =
+ * -inf.  max_new: no sequence has more new tokens (cu NULL: T / B).
  * workspace: used by one call at a time; may be NULL where none is needed.  o
  * and lse must not overlap q.  One kernel, or two. */
 int fp4attn_kv_attention(const fp4attn_kv_cache_t *cache, const fp4attn_kv_batch_t *batch, const void *q,

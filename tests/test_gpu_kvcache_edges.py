@@ -39,3 +39,50 @@ def test_prompts_that_alternate_give_the_same_bits(fa, D):
     assert np.all(np.abs(want[0][0].double().cpu().numpy() - o) <= to)
     assert np.all(np.abs(want[0][1].double().cpu().numpy() - lse) <= tl)
     assert all(torch.all(torch.isfinite(o)) for o, _ in want)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("news,columns", [([1, 3], 0), ([1, 3], WIDE), ([70, 90], 0)])
+@pytest.mark.parametrize("k_exp,scale,window", [(-32, 1.0, 0), (-28, 1.0, 40), (32, 1.0, 0), (0, 1e-9, 0), (-10, 1e-6, 40)])
+def test_zero_and_tiny_rows_at_every_scale(fa, D, news, columns, k_exp, scale, window):
+    """A masked score stays masked where the factor from products to scores leaves fp32's normal numbers."""
+    s = Setup(fa, [150, 90], news, D=D, seed=3, k_exp=k_exp, v_exp=k_exp, kv_scale=2.0 ** k_exp, columns=columns)
+    q = s.queries(2, 2.0 ** -k_exp)
+    q[0], q[2, 1] = 0, 0
+    q[1] *= 2.0 ** -80
+    q[3, 0] *= 2.0 ** -60
+    scale *= D ** -0.5
+    kw = dict(window=window) if window else {}
+    check_attention(fa, s, 2, q=q, scale=scale, **kw)
+    common = dict(cu=s.d_cu, max_new=max(news), softmax_scale=scale, window=window)
+    _, lse = fa.kv_attention(q.cuda(), s.cache, s.d_table, s.d_lens, **common)
+    w = torch.zeros((s.B, s.H, s.M * 64), device="cuda")
+    fa.kv_accumulate(q.cuda(), lse, w, s.cache, s.d_table, s.d_lens, **common)
+    ok(fa)
+    rw = np.zeros(w.shape)
+    tw = ref.attention(q.double().numpy(), s.pool, s.table, s.lens, s.cu, D, k_exp, k_exp, scale, weights=rw,
+                       lse_in=lse.double().cpu().numpy(), window=window)[4]
+    assert np.all(np.abs(w.double().cpu().numpy() - rw) <= tw)
+
+
+@pytest.mark.parametrize("news", [[1, 3], [70, 90]])
+@pytest.mark.parametrize("cap,scale", [(2.0 ** 90, 1.0), (1e20, 1.0), (1e20, 2.0 ** -100)])
+def test_caps_far_above_the_scores_change_nothing(fa, news, cap, scale):
+    """c tanh(s / c) is s to (s / c)^2 / 3 of itself.  The kernel's tanh adds 2^-21 of each score."""
+    s = Setup(fa, [150, 90], news, D=128, seed=3)
+    s.append_all()
+    s.store_all()
+    q = s.queries(2, 1 / scale)
+    scale *= 128 ** -0.5
+    o, lse = fa.kv_attention(q.cuda(), s.cache, s.d_table, s.d_lens, cu=s.d_cu, max_new=max(news), softmax_scale=scale,
+                             softcap=cap)
+    ok(fa)
+    ro, rl, to, tl = ref.attention(q.double().numpy(), s.pool, s.table, s.lens, s.cu, 128, s.k_exp, s.v_exp, scale,
+                                   prompt=max(news) > 3)
+    most = max(np.abs(ref.gather(s.pool, s.table, b, s.lens[b], h, 128, s.k_exp, s.v_exp)[0]
+                      @ q[s.cu[b]:s.cu[b + 1], 2 * h:2 * h + 2].double().numpy().reshape(-1, 128).T).max() * scale
+               for b in range(2) for h in range(s.H))
+    ds = 2.0 ** -21 * most
+    vmax = float(torch.cat(s.v).abs().max()) * 1.2  # (stored values are off by a sixth at most)
+    assert np.all(np.abs(o.double().cpu().numpy() - ro) <= to + 2 * ds * vmax)
+    assert np.all(np.abs(lse.double().cpu().numpy() - rl) <= tl + ds)

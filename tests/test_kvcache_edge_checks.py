@@ -1,0 +1,39 @@
+"""Refusals of the cache calls at the edges of what they accept, on the CPU (host memory stands in for device buffers;
+every refusal comes before a launch)."""
+import ctypes
+
+import pytest
+import torch
+
+from test_kvcache_checks import B, D, G, H, M, P, bf16, cache, calls, fa, i32  # noqa: F401 (fa: fixture)
+
+
+@pytest.fixture
+def library(fa):
+    """(attention, accumulate) of the library, as functions of what a case changes."""
+    from blackwell_nvfp4_quantize_gb300 import kvcache as kv
+
+    L = kv._L()
+    buf = ctypes.create_string_buffer(4096)
+    at = (ctypes.addressof(buf) + 255) // 256 * 256
+
+    def query_args(k_exp=0, heads=H, rows=B, sequences=B, max_pages=M, cu=None, group=G, max_new=1, scale=0.1, cap=0.0):
+        return (kv._Cache(at, P, heads, D, k_exp, 0), kv._Batch(at, at, cu, sequences, max_pages, rows), at, H * G * D, D,
+                group, max_new, scale, cap, 0, None)
+
+    def attention(**kw):
+        return L.fp4attn_kv_attention(*query_args(**kw), at, at, at, 1 << 40, None), buf
+
+    def accumulate(**kw):
+        return L.fp4attn_kv_accumulate(*query_args(**kw), at, at, 1 << 20, 1.0, None), buf
+
+    return lambda **kw: (attention(**kw)[0], accumulate(**kw)[0])
+
+
+def test_factors_that_fp32_does_not_hold(fa, library):
+    bad = (fa.FP4ATTN_ERR_INVALID_ARG,) * 2
+    # scores' factor below fp32's normal numbers; caps that would push it there, or overflow
+    for kw in (dict(scale=1e-39), dict(k_exp=-32, scale=1e-30), dict(cap=2.0 ** 91), dict(cap=3e38)):
+        assert library(**kw) == bad, kw
+    for kw in (dict(k_exp=-32, scale=1e-28), dict(cap=2.0 ** 90), dict(cap=2.0 ** 90, scale=1e-30)):
+        assert library(rows=0, max_new=0, **kw) == (fa.FP4ATTN_OK,) * 2, kw
