@@ -579,12 +579,12 @@ __global__ void __launch_bounds__(kAttnThreads, resident(D, NT)) kv_attn_kernel(
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           uint32_t s01 = e4m3x2_to_half2(vs[i]), s89 = e4m3x2_to_half2(vs[i] >> 16);
-          if (live < kPage) {  // what lies behind the last token may be anything: P is 0 there, V must be finite
-            const int t = 16 * (i0 + i) + 2 * c;
-            if (t >= live) s01 &= 0xFFFF0000u;
-            if (t + 1 >= live) s01 &= 0xFFFFu;
-            if (t + 8 >= live) s89 &= 0xFFFF0000u;
-            if (t + 9 >= live) s89 &= 0xFFFFu;
+          if (hides) {  // what lies behind the last token or before every window may be anything: P is 0, V must be finite
+            const int t = 16 * (i0 + i) + 2 * c, gone = p.window > 0 ? q.at_min - p.window + 1 - slot0 : 0;
+            if (t >= live || t < gone) s01 &= 0xFFFF0000u;
+            if (t + 1 >= live || t + 1 < gone) s01 &= 0xFFFFu;
+            if (t + 8 >= live || t + 8 < gone) s89 &= 0xFFFF0000u;
+            if (t + 9 >= live || t + 9 < gone) s89 &= 0xFFFFu;
           }
           const uint8_t* va = page + PageLayout<D>::kVc + ((2 * (i0 + i)) * 8 + g) * (D / 2) + c * (D / 8);
           const uint8_t* vb = va + 8 * (D / 2);

@@ -450,9 +450,11 @@ int fp4attn_fwd_host_batch(int nsteps, const void *const *q_h, const void *const
  * sequence with more new tokens than max_new is skipped (a page counts as
  * unseen, a sequence's rows stay as they were) and reported by
  * fp4attn_device_status as FP4ATTN_ERR_BAD_INDEX.  Table entries behind a
- * sequence's last page are not read.  Sequences may share pages of tokens that
- * are already written; a page that receives new tokens belongs to one.  At most
- * 2048 sequences, 2^24 pages per sequence and 2^28 rows per call. */
+ * sequence's last page are not read, nor does attention (or the gathering of
+ * weight) read those of pages before the windows of all its queries, or let
+ * what else lies outside their reach count.  Sequences may share pages of
+ * tokens that are already written; a page that receives new tokens belongs to
+ * one.  At most 2048 sequences, 2^24 pages per sequence and 2^28 rows per call. */
 typedef struct {
     uint8_t *pages; /* [num_pages, heads, 72 D], 16-byte aligned */
     int num_pages;

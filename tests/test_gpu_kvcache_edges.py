@@ -86,3 +86,31 @@ def test_caps_far_above_the_scores_change_nothing(fa, news, cap, scale):
     vmax = float(torch.cat(s.v).abs().max()) * 1.2  # (stored values are off by a sixth at most)
     assert np.all(np.abs(o.double().cpu().numpy() - ro) <= to + 2 * ds * vmax)
     assert np.all(np.abs(lse.double().cpu().numpy() - rl) <= tl + ds)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("news,columns", [([3, 2], 0), ([3, 2], WIDE), ([70, 90], 0)])
+@pytest.mark.parametrize("window", [1, 20, 64, 130])
+def test_pages_before_the_window_may_be_gone(fa, D, news, columns, window):
+    """What every query's window has left behind is not looked at: pages may be back in the pool (-1 in the table, or
+    in use by others), what shares a page with visible tokens may hold NaN scales."""
+    s = Setup(fa, [500, 333], news, D=D, seed=5, columns=columns)
+    s.append_all()
+    q = s.queries(2).cuda()
+    want = rows_alone(fa, s, q, window=window)
+    lse0 = want[1].clone()
+    w = [torch.zeros((2, s.H, s.M * 64), device="cuda") for _ in range(2)]
+    common = dict(cu=s.d_cu, max_new=max(news), window=window)
+    fa.kv_accumulate(q, lse0, w[0], s.cache, s.d_table, s.d_lens, **common)
+    ok(fa)
+    for b, (L, n) in enumerate(zip(s.lens, news)):
+        first = L - n - window + 1  # the first slot that some query sees
+        for slot in range(first // 64 * 64, first):
+            for h in range(s.H):
+                for at in ref.offsets(slot % 64, D):
+                    s.cache.pages[int(s.table[b, slot // 64]), h, torch.from_numpy(at).cuda()] = 0xFF
+        s.d_table[b, :first // 64] = torch.tensor([-1, s.P] * 8, device="cuda")[:first // 64]
+    o, lse = rows_alone(fa, s, q, window=window)
+    fa.kv_accumulate(q, lse0, w[1], s.cache, s.d_table, s.d_lens, **common)
+    ok(fa)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and torch.equal(w[0], w[1])
