@@ -13,6 +13,10 @@ One step of generation::
 
 A prompt or drafted tokens take the same calls with several rows per sequence
 (``cu``: int32 [B + 1] row offsets; without it every sequence has T / B rows).
+
+With ``stream`` (a torch stream or a handle) a call runs on that stream.  Its
+inputs have to be ready there, and whoever reads its results on another stream
+waits for it, as with torch's own operations.
 """
 from __future__ import annotations
 
@@ -173,8 +177,7 @@ def _check_out(t, name, dtype, shape, dev):
 
 
 def _stream_of(stream, dev):
-    """(handle, torch stream or None): memory made for a call on a given stream belongs to that stream too.  The
-    last check of every call."""
+    """(handle, torch stream or None: the current one).  The last check of every call."""
     if dev < 0:
         raise ValueError("the cache must be on a CUDA device")
     if stream is None:
@@ -184,14 +187,25 @@ def _stream_of(stream, dev):
         stream = torch.cuda.ExternalStream(int(stream), device=device) if stream else torch.cuda.default_stream(device)
     elif stream.device.index != dev:
         raise ValueError("stream belongs to %s, the cache to cuda:%d" % (stream.device, dev))
-    return stream.cuda_stream, stream
+    handle = stream.cuda_stream
+    return handle, None if handle == _raw_stream(dev) else stream
+
+
+def _scratch(shape, dtype, dev, side):
+    """Memory that the call alone uses.  What a side stream writes comes from that stream's memory: a block of the
+    current stream may still be in use by kernels that the side stream does not wait for."""
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(side):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _new(shape, dtype, dev, side):
-    """An output made by the call; one for a side stream is not reused before that stream is past it."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
+    """An output made by the call; one of a side stream is not reused there before the current stream, whose caller
+    gets it, is past it."""
+    t = _scratch(shape, dtype, dev, side)
     if side is not None:
-        t.record_stream(side)
+        t.record_stream(torch.cuda.current_stream(dev))
     return t
 
 
@@ -301,7 +315,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: tor
     if workspace is None:
         need, ws_at = _workspace_of(dev, heads, D, B, M, group, max_new), None
         if need:
-            workspace = _new((need,), _u8, dev, side)
+            workspace = _scratch((need,), _u8, dev, side)
             ws_at = workspace.data_ptr()
     else:
         need, ws_at = workspace.numel(), workspace.data_ptr()

@@ -114,3 +114,51 @@ def test_pages_before_the_window_may_be_gone(fa, D, news, columns, window):
     fa.kv_accumulate(q, lse0, w[1], s.cache, s.d_table, s.d_lens, **common)
     ok(fa)
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and torch.equal(w[0], w[1])
+
+
+def stream_calls(fa, s, q, big):
+    """Every call that makes its outputs, for a given stream."""
+    w = torch.rand((2, s.H, s.M * 64), device="cuda")
+    nt = torch.from_numpy(s.spare[:4].reshape(2, 2).copy()).cuda()
+    cu = torch.tensor([0, 60, 100], dtype=torch.int32, device="cuda")
+    return {
+        "read": lambda st: fa.kv_read(s.cache, s.d_table, s.d_lens, 100, cu=cu, stream=st),
+        "attention": lambda st: fa.kv_attention(q, s.cache, s.d_table, s.d_lens, stream=st),
+        "prompt": lambda st: fa.kv_attention(big, s.cache, s.d_table, s.d_lens, cu=cu, max_new=60, stream=st),
+        "evict": lambda st: fa.kv_evict(s.cache, w, s.d_table, s.d_lens, nt, 66, stream=st),
+    }
+
+
+@pytest.mark.parametrize("name", ["read", "attention", "prompt", "evict"])
+@pytest.mark.parametrize("columns", [0, WIDE])
+@pytest.mark.parametrize("handle", [False, True])
+def test_memory_of_a_call_on_another_stream(fa, name, columns, handle):
+    """Neither do kernels of the current stream that are still to come write to the memory that a call on another
+    stream gets, nor does the next such call get memory that the current stream still reads."""
+    s = Setup(fa, [700, 190], [1, 1], seed=2, spare=6, columns=columns)
+    s.append_all()
+    q, big = (Setup._bf16(s.rng.standard_normal((n, 4, s.D))).cuda() for n in (2, 100))
+    call = stream_calls(fa, s, q, big)[name]
+    want = call(None)
+    side = torch.cuda.Stream()
+    st = side.cuda_stream if handle else side
+    ok(fa)
+    sizes = [x.numel() * x.element_size() for x in want] + [1 << 20, 1 << 22, 1 << 24, 1 << 26]
+    junk = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(2)]
+    torch.cuda._sleep(400_000_000)
+    for x in junk:
+        x.fill_(0x7F)  # after the sleep
+    del junk, x
+    got = call(st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # read late on the current stream, while the other one goes on
+    torch.cuda._sleep(400_000_000)
+    late = [x.clone() for x in got]
+    del got
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            for x in call(st):
+                x.fill_(3)
+    ok(fa)
+    assert all(torch.equal(a, b) for a, b in zip(late, want))
