@@ -102,32 +102,31 @@ __device__ __forceinline__ void tc_commit2(uint32_t bar) {
       : "memory");
 }
 
-// Dynamic shared memory begins here (the system's first KB lies before it): the
-// MMAs' descriptors and barriers are then constants.  The issuing warp shares
-// its scheduler with two of the rows' warps, which leave it one slot in three
-// or four, so what it executes per MMA (32 to 64 cycles apart) has to be
-// little.  A kernel that finds another address reports it and does nothing.
-constexpr uint32_t kSmemBase = 1024;
-__host__ __device__ constexpr uint64_t desc_const(uint32_t offset) {
-  return ((kSmemBase + offset) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
+// The issuing warp shares its scheduler with two of the rows' warps, which leave
+// it one slot in three or four, so what it executes per MMA (32 to 64 cycles
+// apart) has to be little.  Descriptors are constants plus the address of shared
+// memory, added to their low word in the batch (added outside, for every stage
+// and tile, they would all be kept in registers, and spill).
+__host__ __device__ constexpr uint32_t desc_low(uint32_t offset) { return (offset >> 4) | (1u << 16); }
+constexpr uint32_t kDescHigh = 64u | (1u << 14) | (2u << 29);
 
 // M = 256 over the CTA pair: A and D rows 128 in each CTA (the same offsets), B
 // rows N / 2 in each.  The whole warp comes here with operands that are
 // constants; one lane, elected once per batch, issues the MMAs of a batch and
 // the commit that reports them to both CTAs.
 // S of tile T, page PG of stage S (32 key rows of the page in each CTA)
+// (base: shared memory's address / 16, the same in both CTAs)
 template <int D, int T, int PG, int S>
-__device__ __forceinline__ void issue_qk(uint32_t s_full) {
+__device__ __forceinline__ void issue_qk(uint32_t base, uint32_t s_full) {
   using L_ = PromptSmem<D>;
   constexpr uint32_t d = kColS + 128 * T + kPage * PG, id = idesc_f16(256, kPage);
-  constexpr uint64_t a = desc_const(L_::kQ + T * L_::kQTile), b = desc_const(L_::kK + S * L_::kKTile + PG * (32 * 128));
+  constexpr uint32_t a = desc_low(L_::kQ + T * L_::kQTile), b = desc_low(L_::kK + S * L_::kKTile + PG * (32 * 128));
   // to the next 64 channels
   constexpr uint64_t da = 128 * 128 / 16 - 6, db = kPage * 128 / 16 - 6;
   if constexpr (D == 128) {
     asm volatile(
-      "{\n.reg .pred e, f, t;\n.reg .b64 a, b;\n.reg .b16 m;\nelect.sync _|e, 0xffffffff;\n"
-      "setp.ne.b32 f, 0, 0;\nsetp.eq.b32 t, 0, 0;\nmov.b64 a, %1;\nmov.b64 b, %2;\n"
+      "{\n.reg .pred e, f, t;\n.reg .b64 a, b;\n.reg .b32 lo;\n.reg .b16 m;\nelect.sync _|e, 0xffffffff;\n"
+      "setp.ne.b32 f, 0, 0;\nsetp.eq.b32 t, 0, 0;\nadd.u32 lo, %7, %1;\nmov.b64 a, {lo, %8};\nadd.u32 lo, %7, %2;\nmov.b64 b, {lo, %8};\n"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, f;\n"
       "add.s64 a, a, 2;\nadd.s64 b, b, 2;\n"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n"
@@ -143,13 +142,13 @@ __device__ __forceinline__ void issue_qk(uint32_t s_full) {
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n"
       "add.s64 a, a, 2;\nadd.s64 b, b, 2;\n"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n"
-      "mov.b16 m, 3;\n@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%6], m;\n}\n"
-        ::"r"(d), "l"(a), "l"(b), "r"(id), "n"(da), "n"(db), "r"(s_full + 8 * (2 * T + PG))
+      "mov.b16 m, 3;\n@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%6 + %9], m;\n}\n"
+        ::"r"(d), "n"(a), "n"(b), "r"(id), "n"(da), "n"(db), "r"(s_full), "r"(base), "n"(kDescHigh), "n"(8 * (2 * T + PG))
         : "memory");
   } else {
     asm volatile(
-      "{\n.reg .pred e, f, t;\n.reg .b64 a, b;\n.reg .b16 m;\nelect.sync _|e, 0xffffffff;\n"
-      "setp.ne.b32 f, 0, 0;\nsetp.eq.b32 t, 0, 0;\nmov.b64 a, %1;\nmov.b64 b, %2;\n"
+      "{\n.reg .pred e, f, t;\n.reg .b64 a, b;\n.reg .b32 lo;\n.reg .b16 m;\nelect.sync _|e, 0xffffffff;\n"
+      "setp.ne.b32 f, 0, 0;\nsetp.eq.b32 t, 0, 0;\nadd.u32 lo, %7, %1;\nmov.b64 a, {lo, %8};\nadd.u32 lo, %7, %2;\nmov.b64 b, {lo, %8};\n"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, f;\n"
       "add.s64 a, a, 2;\nadd.s64 b, b, 2;\n"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n"
@@ -157,20 +156,20 @@ __device__ __forceinline__ void issue_qk(uint32_t s_full) {
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n"
       "add.s64 a, a, 2;\nadd.s64 b, b, 2;\n"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n"
-      "mov.b16 m, 3;\n@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%6], m;\n}\n"
-        ::"r"(d), "l"(a), "l"(b), "r"(id), "n"(da), "n"(db), "r"(s_full + 8 * (2 * T + PG))
+      "mov.b16 m, 3;\n@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%6 + %9], m;\n}\n"
+        ::"r"(d), "n"(a), "n"(b), "r"(id), "n"(da), "n"(db), "r"(s_full), "r"(base), "n"(kDescHigh), "n"(8 * (2 * T + PG))
         : "memory");
   }
 }
 // O of tile T += P V of page PG of stage S
 template <int D, int T, int PG, int S>
-__device__ __forceinline__ void issue_pv(uint32_t o_full, bool acc) {
+__device__ __forceinline__ void issue_pv(uint32_t base, uint32_t o_full, bool acc) {
   using L_ = PromptSmem<D>;
   constexpr uint32_t d = kColO + 128 * T, a = kColS + 128 * T + kPage * PG, id = idesc_f16(256, D);
-  constexpr uint64_t b = desc_const(L_::kV + S * L_::kVTile + PG * ((D / 2) * 128));
+  constexpr uint32_t b = desc_low(L_::kV + S * L_::kVTile + PG * ((D / 2) * 128));
   asm volatile(
-      "{\n.reg .pred e, f, t;\n.reg .b64 b;\n.reg .b32 a;\n.reg .b16 m;\nelect.sync _|e, 0xffffffff;\n"
-      "setp.ne.b32 f, %4, 0;\nsetp.eq.b32 t, 0, 0;\nmov.b32 a, %1;\nmov.b64 b, %2;\n"
+      "{\n.reg .pred e, f, t;\n.reg .b64 b;\n.reg .b32 a, lo;\n.reg .b16 m;\nelect.sync _|e, 0xffffffff;\n"
+      "setp.ne.b32 f, %4, 0;\nsetp.eq.b32 t, 0, 0;\nmov.b32 a, %1;\nadd.u32 lo, %6, %2;\nmov.b64 b, {lo, %7};\n"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %3, f;\n"
       "add.s32 a, a, 8;\nadd.s64 b, b, 2;\n"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %3, t;\n"
@@ -178,8 +177,8 @@ __device__ __forceinline__ void issue_pv(uint32_t o_full, bool acc) {
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %3, t;\n"
       "add.s32 a, a, 8;\nadd.s64 b, b, 2;\n"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %3, t;\n"
-      "mov.b16 m, 3;\n@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5], m;\n}\n"
-      ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(acc ? 1 : 0), "r"(o_full + 8 * (2 * T + PG))
+      "mov.b16 m, 3;\n@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5 + %8], m;\n}\n"
+      ::"r"(d), "r"(a), "n"(b), "r"(id), "r"(acc ? 1 : 0), "r"(o_full), "r"(base), "n"(kDescHigh), "n"(8 * (2 * T + PG))
       : "memory");
 }
 // f with stage s as a constant
@@ -317,7 +316,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
   __syncthreads();
   cluster_sync();  // the other CTA's barriers are there
   tc_fence_after();
-  // the only CTA on the SM holds all 512 columns, so they start at column 0
+  // (an allocation of all 512 columns begins at column 0)
   const uint32_t tmem_base = *tmem_slot;
   chain_wait();
   chain_next();
@@ -330,11 +329,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
     if (warp == kWarpMma) tmem_dealloc2(tmem_base, 512);
     return;
   }
-  const bool as_planned = tmem_base == 0 && (smem_u32(smem) & 0xFFFFFFu) == kSmemBase;  // (above: the CTA's rank)
-  if (!as_planned) {
-    if (threadIdx.x == 0 && atomicCAS(&p.g.status->timeout, 0u, 1u) == 0u) p.g.status->where = 71;
-    if (rank == 0 && threadIdx.x == 0) split_of(p, pair)->last = -1;  // nothing to join
-  } else if (warp < kWarpDq) {
+  if (warp < kWarpDq) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
     // ---------------------------------------------------------------- softmax
     const int t = warp >> 2, row = threadIdx.x & 127;
@@ -782,9 +777,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
         // -------------------------------------------------------------- MMA
         int k = 0, nk[2] = {0, 0}, ns[2] = {0, 0};  // blocks of the pair; blocks and segments of each tile
         bool ok = true;
-        constexpr uint32_t kBarBase = kSmemBase + L_::kBars;  // the barriers in the order above
-        constexpr uint32_t bKEmpty = kBarBase + 8 * (2 + kStages + 4), bVEmpty = bKEmpty + 8 * kStages;
-        constexpr uint32_t bS = bVEmpty + 8 * kStages, bO = bS + 8 * 4, bDrain = bO + 8 * 4;
+        const uint32_t bKEmpty = smem_u32(k_empty), bVEmpty = smem_u32(v_empty), bS = smem_u32(s_full), bO = smem_u32(o_full);
+        const uint32_t base = (smem_u32(smem) & 0x3FFFFu) >> 4;
         auto wait_for = [&](auto smem_too, uint64_t* bar, int phase, unsigned site) {
           ok = ok && bounded_wait([&]() { return pair_try_wait<smem_too.value>(bar, phase & 1); }, abort_flag, p.g.status, site);
           ok = __all_sync(0xFFFFFFFFu, ok);
@@ -801,10 +795,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
           if (two) wait(q_full + 1, ns[1]++, 78);
           if (!ok) break;
           by_stage(k % kStages, [&](auto s) {
-            issue_qk<D, 0, 0, s.value>(bS);
-            if (two) issue_qk<D, 1, 0, s.value>(bS);
-            issue_qk<D, 0, 1, s.value>(bS);
-            if (two) issue_qk<D, 1, 1, s.value>(bS);
+            issue_qk<D, 0, 0, s.value>(base, bS);
+            if (two) issue_qk<D, 1, 0, s.value>(base, bS);
+            issue_qk<D, 0, 1, s.value>(base, bS);
+            if (two) issue_qk<D, 1, 1, s.value>(base, bS);
             tc_commit2(bKEmpty + 8 * s.value);
           });
           for (int j = 0; j < nblk && ok; ++j, ++k, ++nk[0], nk[1] += two) {
@@ -816,32 +810,32 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
               // page 0 of the tiles, then page 1: P in, the page's S of the next block out
               wait_p(p_full, nk[0]);
               if (!ok) return;
-              issue_pv<D, 0, 0, S>(bO, j > 0);
-              if (more) issue_qk<D, 0, 0, S1>(bS);
+              issue_pv<D, 0, 0, S>(base, bO, j > 0);
+              if (more) issue_qk<D, 0, 0, S1>(base, bS);
               if (two) {
                 wait_p(p_full + 2, nk[1]);
                 if (!ok) return;
-                issue_pv<D, 1, 0, S>(bO, j > 0);
-                if (more) issue_qk<D, 1, 0, S1>(bS);
+                issue_pv<D, 1, 0, S>(base, bO, j > 0);
+                if (more) issue_qk<D, 1, 0, S1>(base, bS);
               }
               wait_p(p_full + 1, nk[0]);
               if (!ok) return;
-              issue_pv<D, 0, 1, S>(bO, true);
+              issue_pv<D, 0, 1, S>(base, bO, true);
               if (!two) tc_commit2(bVEmpty + 8 * S);
-              if (more) issue_qk<D, 0, 1, S1>(bS);
+              if (more) issue_qk<D, 0, 1, S1>(base, bS);
               if (two) {
                 wait_p(p_full + 3, nk[1]);
                 if (!ok) return;
-                issue_pv<D, 1, 1, S>(bO, true);
+                issue_pv<D, 1, 1, S>(base, bO, true);
                 tc_commit2(bVEmpty + 8 * S);
-                if (more) issue_qk<D, 1, 1, S1>(bS);
+                if (more) issue_qk<D, 1, 1, S1>(base, bS);
               }
               if (more) tc_commit2(bKEmpty + 8 * S1);
             });
           }
           u = seg_end;
         }
-        tc_commit2(bDrain);
+        tc_commit2(smem_u32(drain));
       }
     } else if (rank == 1) {
       // ------------------------------------------------------ passing on
@@ -872,7 +866,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
   tc_fence_before();
   __syncthreads();
   // no operation of the pair is in flight when it frees its columns
-  if (warp == kWarpMma && as_planned) mbar_wait_drain(drain, 0, abort_flag, p.g.status, 82);
+  if (warp == kWarpMma) mbar_wait_drain(drain, 0, abort_flag, p.g.status, 82);
   cluster_sync();  // neither CTA leaves while the other's MMAs read it
   tc_fence_after();
   if (warp == kWarpMma) tmem_dealloc2(tmem_base, 512);

@@ -162,3 +162,19 @@ def test_memory_of_a_call_on_another_stream(fa, name, columns, handle):
                 x.fill_(3)
     ok(fa)
     assert all(torch.equal(a, b) for a, b in zip(late, want))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompts_write_every_row(fa, D):
+    """No row of a sequence is left as it was, whatever the batch (the size of the largest moves the kernel's shared
+    memory about)."""
+    for B in (1, 3, 130, 2048):
+        news = [70 if b % 700 == 0 else 1 for b in range(B)]
+        s = Setup(fa, news, news, H=1, D=D, seed=B)
+        s.append_all()
+        q = s.queries(1).cuda()
+        o = torch.full(q.shape, 1000.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full(q.shape[:2], 1000.0, device="cuda")
+        rows_alone(fa, s, q, o=o, lse=lse)
+        ok(fa)
+        assert torch.all(o.abs() < 100) and torch.all(lse.abs() < 100)
