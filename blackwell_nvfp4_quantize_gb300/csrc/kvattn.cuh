@@ -176,6 +176,7 @@ __device__ __forceinline__ float join_factor(float m, float top) { return top ==
 // one, `last` (-1: the run has none; at most one begins in each).
 struct Split {
   int last, row0, h, r0, r1;
+  float shift;  // P was held as 2^shift p
 };
 __device__ __forceinline__ Split* split_of(const KvAttnParams& p, int run) { return reinterpret_cast<Split*>(p.plan) + run; }
 
@@ -190,7 +191,7 @@ template <int D>
 constexpr int kJoinRows = kJoinThreads / (D / 4) * kDeep;  // of a block
 
 template <int D, int kCols>
-__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvAttnParams p, float shift) {
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvAttnParams p) {
   constexpr int kLanes = D / 4, kRows = kJoinThreads / kLanes, kPart = part_floats<D>(kCols);
   chain_start();
   const int c0 = blockIdx.x, lane = threadIdx.x % kLanes, col0 = blockIdx.y * kJoinRows<D> + threadIdx.x / kLanes;
@@ -249,11 +250,11 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvAttnParam
     const __nv_bfloat162 hi = __floats2bfloat162_rn(out_o(acc[i].z, sum[i], p.v_up), out_o(acc[i].w, sum[i], p.v_up));
     *reinterpret_cast<uint2*>(p.o + out * D + 4 * lane) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    if (lane == 0) p.lse[out] = out_lse(top[i], sum[i], shift);
+    if (lane == 0) p.lse[out] = out_lse(top[i], sum[i], x.shift);
   }
 }
 
-// The plan's part of a workspace, before the partial results (the splits of up to 400 runs of the prompt kernel).
+// The plan's part of a workspace, before the partial results (the splits of up to 340 runs of the prompt kernel).
 inline size_t plan_bytes() { return (static_cast<size_t>(kMaxKvBatch + 1) * 4 + 255) / 256 * 256; }
 
 // Attention of many queries (kvprompt.cu): runs (CTA pairs), workspace, launch.

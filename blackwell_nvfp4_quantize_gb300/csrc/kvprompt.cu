@@ -47,9 +47,14 @@
 // which 32 remain with a window of one token: start, join, and for each of the 2
 // or 3 problems of a pair its queries, first scores and results.
 //
-// P is held as 2^3 p against a reference maximum that may lag by 2^12 (moving it
-// costs a pass over O in TMEM), so that its largest value is 2^15, and what
-// falls below 2^-28 of the reference is dropped; its sum is kept of the fp32 values before they are rounded to fp16.
+// P is held as 2^(15 - slack) p against a reference maximum that may lag by
+// 2^slack (moving it costs a pass over O in TMEM), so that its largest value is
+// 2^15.  fp16 is off by 2^-25 at most down there, 2^(slack - 40) of the
+// reference, and drops what is smaller; the sum of P is kept of the fp32 values
+// before they are rounded.  L tokens together then lose L 2^(slack - 40) of the
+// largest |V| at most: the slack is 12 up to 2^17 tokens, where that is 2^-11
+// (a quarter of bf16's rounding), and one less with every further doubling, down
+// to 1.  (A slack of 8 for all costs 3%: prompt_chunk 984 us, of 4 992.)
 #include <type_traits>
 
 #include "kvattn.cuh"
@@ -68,8 +73,9 @@ constexpr int kWarpDq = 8, kWarpMma = 12;
 constexpr int kPromptThreads = 512;
 constexpr int kRegsRows = 176, kRegsOperands = 96, kRegsMma = 64;
 static_assert(2 * kRegsRows + kRegsOperands + kRegsMma == 4 * 128, "registers of the launch");
-constexpr float kShift = 3.0f;
-constexpr float kSlack = 12.0f;
+constexpr float kPMax = 15.0f;  // P is below 2^kPMax
+// How far the reference maximum of a sequence of L tokens may lag, in powers of two.
+__device__ __forceinline__ float slack_of(int L) { return static_cast<float>(min(12, max(1, __clz(L - 1) - 3))); }
 constexpr uint32_t kColS = 0, kColO = 256;  // tile t: S at 128 t, O at 256 + 128 t
 
 template <int D>
@@ -399,6 +405,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
       const float cs = score_factor<MOD>(p, down);
       const float slope = MOD && p.slopes ? p.slopes[x.h * p.G + r % p.G] * kLog2Ef : 0.0f;
       const float cap = p.cap * kLog2Ef;
+      const float slack = slack_of(x.L), shift = kPMax - slack;
       // S (in TMEM at tp, and in v) -> log2-domain scores; dist: of the first one
       // from the query.  A NaN stays one on either way through the cap.  Scores
       // that are not far below their cap are rare and go through TMEM, so that
@@ -492,7 +499,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
           mt = fmaxf(a0, a1);
         }
         if constexpr (!MOD) mt *= cs;
-        const bool moves = mt > m + kSlack;  // (m = -inf: as soon as something is seen)
+        const bool moves = mt > m + slack;  // (m = -inf: as soon as something is seen)
         if (__any_sync(0xFFFFFFFFu, moves)) {
           const float alpha = moves ? ex2_approx(m - mt) : 1.0f;
           l *= alpha;
@@ -516,7 +523,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
           }
         }
         // P over the columns S came in
-        const float off = kShift - (m == -INFINITY ? 0.0f : m);
+        const float off = shift - (m == -INFINITY ? 0.0f : m);
         const float f = MOD ? 1.0f : cs;
         float l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
@@ -583,7 +590,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
           for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         }
       }
-      if (real && whole) p.lse[out] = out_lse(m, l, kShift);
+      if (real && whole) p.lse[out] = out_lse(m, l, shift);
       if (real && !whole) {
         part[kRowsPair * D + col] = m;
         part[kRowsPair * D + kRowsPair + col] = l;
@@ -860,7 +867,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
       // for the join: the problem that begins in this run and does not end in it
       const Unit x = find_unit<kRowsPair, kBlockKeys>(p, prefix, end - 1);
       const bool split = x.begin >= start && x.end > end;
-      if (lane == 0) *split_of(p, pair) = Split{split ? (x.end - 1) / per : -1, x.row0, x.h, x.r0, x.r1};
+      if (lane == 0) *split_of(p, pair) = Split{split ? (x.end - 1) / per : -1, x.row0, x.h, x.r0, x.r1, kPMax - slack_of(x.L)};
     }
   }
   tc_fence_before();
@@ -879,7 +886,7 @@ cudaError_t launch_d(const KvAttnParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_chained_cluster(kv_prompt_kernel<D, MOD>, dim3(2 * p.ctas), 2, kPromptThreads, L_::bytes(p.g.B), s, p);
   if (e != cudaSuccess) return e;
-  return launch_chained(kv_join_kernel<D, kRowsPair>, dim3(p.ctas, kRowsPair / kJoinRows<D>), kJoinThreads, 0, s, p, kShift);
+  return launch_chained(kv_join_kernel<D, kRowsPair>, dim3(p.ctas, kRowsPair / kJoinRows<D>), kJoinThreads, 0, s, p);
 }
 
 }  // namespace
