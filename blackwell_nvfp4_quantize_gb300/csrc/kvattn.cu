@@ -919,13 +919,20 @@ __global__ void __launch_bounds__(kAttnThreads, 3) kv_weigh_kernel(const KvAttnP
           page_scores<D, NT, 2>(page, i0, ks, q, s);
           scores_of<D, NT, 2, MOD>(p, q, slot0 + 16 * i0 + g, s);
           if (hides) mask_scores<D, NT, 2>(p, q, slot0 + 16 * i0 + g, s);
+          auto add = [&](auto masked) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+              for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                sum[2 * (i0 + i) + (j >> 1)] += ex2_approx(fmaf(s[i][nt][j], MOD ? 1.0f : q.cs[nt][j & 1], -lse[nt][j & 1]));
+                for (int j = 0; j < 4; ++j) {
+                  const float e = ex2_approx(fmaf(s[i][nt][j], MOD ? 1.0f : q.cs[nt][j & 1], -lse[nt][j & 1]));
+                  // (a row whose LSE is no number hands none to a token that it does not see)
+                  sum[2 * (i0 + i) + (j >> 1)] += masked.value && s[i][nt][j] == -INFINITY ? 0.0f : e;
+                }
+          };
+          if (hides) add(std::true_type{});
+          else add(std::false_type{});
         }
       }
       if (x.r1 >= kCols) load(0);

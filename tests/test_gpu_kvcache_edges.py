@@ -208,3 +208,26 @@ def test_a_long_tail_of_light_tokens_counts(fa, D, news):
     ds = (D / 16 + 4 + 4) * 2.0 ** -23 * 19.8
     tol = want * (2.0 ** -8 + 2.0 ** -11 + 2 * (ds + 2.0 ** -21) + 2.0 ** -10) + 2.0 ** -32 * L * v[1].max()
     assert torch.all((o.double().reshape(B, news, G, D) - want).abs() <= tol)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 50])
+def test_weight_of_rows_that_are_not_numbers(fa, D, window):
+    """A query row that is no number spoils the weights of the tokens that it sees, and no others."""
+    s = Setup(fa, [200, 130], [6, 3], D=D, seed=4)
+    s.append_all()
+    q = s.queries(2)
+    q[2, 1, 5] = float("nan")  # the third of six new tokens, first KV head: slots up to 196
+    common = dict(cu=s.d_cu, max_new=6, window=window)
+    good = q.clone()
+    good[2, 1] = 0
+    out = []
+    for x in (q.cuda(), good.cuda()):
+        lse = fa.kv_attention(x, s.cache, s.d_table, s.d_lens, **common)[1]
+        w = torch.zeros((2, s.H, s.M * 64), device="cuda")
+        out.append(fa.kv_accumulate(x, lse, w, s.cache, s.d_table, s.d_lens, **common))
+    ok(fa)
+    spoiled = torch.zeros(out[0].shape, dtype=torch.bool, device="cuda")
+    spoiled[0, 0, 197 - window if window else 0:197] = True
+    assert torch.all(torch.isnan(out[0][spoiled]))
+    assert torch.equal(out[0][~spoiled], out[1][~spoiled])
