@@ -90,6 +90,25 @@ struct RowsParams {
   float k_sixth, v_sixth;                  // append: 2^-exp / 6
 };
 
+// Row offsets that descend or lie outside the tensors: a search for a row's (or
+// a page's) sequence may never come to those, so each is looked at, by thread i
+// of `all`; the first one's offsets are fetched before the search.
+struct OffsetCheck {
+  int i, all, from, to;
+  __device__ __forceinline__ OffsetCheck(const KvGeom& g, int i_, int all_) : i(i_), all(all_), from(0), to(0) {
+    if (g.cu && i < g.B) {
+      from = g.cu[i];
+      to = g.cu[i + 1];
+    }
+  }
+  __device__ __forceinline__ void report(const KvGeom& g) {
+    bool bad = from < 0 || to < from || to > g.T;
+    if (g.cu)
+      for (i += all; i < g.B; i += all) bad |= g.cu[i] < 0 || g.cu[i + 1] < g.cu[i] || g.cu[i + 1] > g.T;
+    if (bad) report_bad_index(g.status);
+  }
+};
+
 // Few rows per sequence: D / 8 lanes per row and head, every part stored where
 // it belongs.  What counts is the chain of dependent loads: 2 us for 8 sequences
 // of one row as for 32 of 8.
@@ -107,7 +126,9 @@ __global__ void __launch_bounds__(kThreads) kv_rows_kernel(const RowsParams p) {
     v = ld_once(p.v + r * p.v_row + h * p.v_head + q * 8);
   }
   int b, slot, pg = -1;
+  OffsetCheck check(p.g, blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads);
   if (in && row_slot(p.g, r, b, slot)) pg = page_of(p.g, b, slot / kPage);
+  check.report(p.g);
   // lanes of a row agree on pg; all lanes reach the shuffles
   const int t = pg >= 0 ? slot & (kPage - 1) : 0;
   uint8_t* page = p.pages + (static_cast<long long>(pg) * p.g.heads + h) * P::kBytes;
@@ -152,6 +173,8 @@ __global__ void __launch_bounds__(kThreads) kv_pages_kernel(const RowsParams p) 
   __shared__ __align__(16) uint8_t buf[2][P::kKBytes];
   const int x = blockIdx.x;
   chain_start();
+  if (p.g.cu && blockIdx.y == 0 && x * kThreads < p.g.B)
+    OffsetCheck(p.g, x * kThreads + threadIdx.x, gridDim.x * kThreads).report(p.g);
   const int per = p.g.cu ? 0 : p.g.T / p.g.B;
   auto base = [&](int b) { return (p.g.cu ? max(p.g.cu[b], 0) : b * per) / kPage + 2 * b; };
   int lo = 0, hi = p.g.B;

@@ -448,7 +448,8 @@ int fp4attn_fwd_host_batch(int nsteps, const void *const *q_h, const void *const
  * that a captured graph can be replayed for longer sequences.  A page outside
  * [0, num_pages), a length outside [0, 64 max_pages], rows outside [0, T) or a
  * sequence with more new tokens than max_new is skipped (a page counts as
- * unseen, a sequence's rows stay as they were) and reported by
+ * unseen, a sequence's rows stay as they were), where row offsets descend some
+ * sequences may be, and each of these is reported by
  * fp4attn_device_status as FP4ATTN_ERR_BAD_INDEX.  Table entries behind a
  * sequence's last page are not read, nor does attention (or the gathering of
  * weight) read those of pages before the windows of all its queries, or let
@@ -467,7 +468,8 @@ typedef struct {
     const int32_t *table; /* [B, max_pages] */
     const int32_t *lens;  /* [B] */
     const int32_t *cu;    /* [B + 1]: sequence b has the rows cu[b] .. cu[b+1] - 1 of the packed tensors;
-                             rows from cu[B] to T are not touched.  NULL: T / B rows each */
+                             the offsets ascend, rows outside cu[0] .. cu[B] - 1 are not touched.  NULL: T / B
+                             rows each */
     int B, max_pages, T;
 } fp4attn_kv_batch_t;
 

@@ -231,3 +231,20 @@ def test_weight_of_rows_that_are_not_numbers(fa, D, window):
     spoiled[0, 0, 197 - window if window else 0:197] = True
     assert torch.all(torch.isnan(out[0][spoiled]))
     assert torch.equal(out[0][~spoiled], out[1][~spoiled])
+
+
+@pytest.mark.parametrize("n", [100, 1000])  # row by row, page by page
+def test_row_offsets_that_do_not_ascend_are_reported(fa, n):
+    """Wherever the descent is, or the row that is not there; the other calls see every sequence anyway."""
+    s = Setup(fa, [6 * n] * 4, [1] * 4, D=64, seed=3)
+    s.append_all()
+    ok(fa)
+    k = torch.zeros((6 * n, s.H, s.D), dtype=torch.bfloat16, device="cuda")
+    for cu in ([0, 5 * n, n, 6 * n, 6 * n], [0, n, 3 * n, 3 * n - 1, 6 * n], [0, 0, n, 6 * n, 5 * n], [n, 0, n, 2 * n, 6 * n],
+               [0, n, -1, n, 6 * n], [0, n, 6 * n + 1, n, 6 * n], [0, n, 6 * n, 6 * n, 6 * n + 3]):
+        at = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        for call in (lambda: fa.kv_append(k, k, s.cache, s.d_table, s.d_lens, cu=at),
+                     lambda: fa.kv_read(s.cache, s.d_table, s.d_lens, 6 * n, cu=at)):
+            call()
+            torch.cuda.synchronize()
+            assert fa.device_status() == fa.FP4ATTN_ERR_BAD_INDEX, cu
