@@ -80,8 +80,8 @@ __device__ __forceinline__ bool seq_of(const KvGeom& p, int b, int& row0, int& n
   return true;
 }
 
-// Sequence and slot of packed row r (r < T): false for rows behind the last
-// sequence and, after a report, for rows whose slot or page is out of range.
+// Sequence and slot of packed row r (r < T): false for rows before the first
+// sequence or behind the last and, after a report, for rows whose slot or page is out of range.
 __device__ __forceinline__ bool row_slot(const KvGeom& p, int r, int& b, int& slot) {
   if (p.cu) {
     int lo = 0, hi = p.B;  // the last b with cu[b] <= r
@@ -90,7 +90,8 @@ __device__ __forceinline__ bool row_slot(const KvGeom& p, int r, int& b, int& sl
       if (p.cu[mid] <= r) lo = mid; else hi = mid;
     }
     b = lo;
-    if (r >= p.cu[p.B]) return false;
+    const int from = p.cu[0];
+    if (r >= p.cu[p.B] || (r < from && from <= p.T)) return false;
   } else {
     b = r / (p.T / p.B);
     if (b >= p.B) return false;

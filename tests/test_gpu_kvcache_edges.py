@@ -248,3 +248,33 @@ def test_row_offsets_that_do_not_ascend_are_reported(fa, n):
             call()
             torch.cuda.synchronize()
             assert fa.device_status() == fa.FP4ATTN_ERR_BAD_INDEX, cu
+
+
+@pytest.mark.parametrize("n", [3, 1000])
+def test_rows_before_the_first_sequence_stay(fa, n):
+    """A part of a longer batch: cu begins past 0."""
+    s = Setup(fa, [n + 70, n + 30], [n, n], D=64, seed=3)
+    s.append_all()
+    ok(fa)
+    pages = s.cache.pages.clone()
+    T = 2 * n + 20
+    cu = torch.tensor([11, 11 + n, 11 + 2 * n], dtype=torch.int32, device="cuda")
+    want = fa.kv_read(s.cache, s.d_table, s.d_lens, 2 * n)
+    out = [torch.full((T, s.H, s.D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    fa.kv_read(s.cache, s.d_table, s.d_lens, T, cu=cu, k=out[0], v=out[1])
+    ok(fa)
+    for x, y in zip(out, want):
+        assert torch.all(x[:11] == 7.0) and torch.all(x[11 + 2 * n:] == 7.0) and torch.equal(x[11:11 + 2 * n], y)
+    new = [torch.cat([torch.cat([torch.full((11, s.H, s.D), 9.0)] + [x[b][L - n:].float() for b, L in enumerate(s.lens)])
+                      , torch.full((9, s.H, s.D), 9.0)]).bfloat16().cuda() for x in (s.k, s.v)]
+    fa.kv_append(new[0], new[1], s.cache, s.d_table, s.d_lens, cu=cu)  # the same rows again
+    ok(fa)
+    assert torch.equal(s.cache.pages, pages)
+    if n == 3:
+        q = Setup._bf16(s.rng.standard_normal((T, 4, s.D))).cuda()
+        want = fa.kv_attention(q[11:17], s.cache, s.d_table, s.d_lens)
+        o, lse = torch.full_like(q, 3.0), torch.full((T, 4), 5.0, device="cuda")
+        fa.kv_attention(q, s.cache, s.d_table, s.d_lens, cu=cu, max_new=3, o=o, lse=lse)
+        ok(fa)
+        assert torch.equal(o[11:17], want[0]) and torch.equal(lse[11:17], want[1])
+        assert torch.all(o[:11] == 3.0) and torch.all(o[17:] == 3.0) and torch.all(lse[:11] == 5.0)
