@@ -1053,10 +1053,10 @@ int check_attn(const fp4attn_kv_cache_t* c, const fp4attn_kv_batch_t* b, const v
   if (!std::isnormal(up) || (cap > 0.0f && !std::isfinite(up / cap))) return FP4ATTN_ERR_INVALID_ARG;
   if (b->T > 0 && (!q || !aligned16(q) || ((q_row | q_head) & 7))) return FP4ATTN_ERR_INVALID_ARG;
   if (static_cast<long long>(c->heads) * group > 65535) return FP4ATTN_ERR_UNSUPPORTED;
-  // units of all tiles must stay within 32 bits
+  // units of all tiles must stay within 32 bits, rounded up to whole runs too
   const long long cols = static_cast<long long>(max_new) * group;
   if (cols > (1ll << 24)) return FP4ATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>(b->B) * c->heads * ((cols + 7) / 8) >= (1ll << 31) / b->max_pages) return FP4ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(b->B) * c->heads * ((cols + 7) / 8) >= (1ll << 30) / b->max_pages) return FP4ATTN_ERR_UNSUPPORTED;
   return FP4ATTN_OK;
 }
 

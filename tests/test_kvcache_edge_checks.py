@@ -37,3 +37,12 @@ def test_factors_that_fp32_does_not_hold(fa, library):
         assert library(**kw) == bad, kw
     for kw in (dict(k_exp=-32, scale=1e-28), dict(cap=2.0 ** 90), dict(cap=2.0 ** 90, scale=1e-30)):
         assert library(rows=0, max_new=0, **kw) == (fa.FP4ATTN_OK,) * 2, kw
+
+
+def test_work_that_32_bits_do_not_count(fa, library):
+    """Units of all tiles, and the runs they are rounded up to, are counted in 32 bits."""
+    uns = (fa.FP4ATTN_ERR_UNSUPPORTED,) * 2
+    # 337 sequences of 6223 KV heads and 1024 pages: 2^31 - 1024 units
+    assert library(sequences=337, rows=337, heads=6223, max_pages=1024, group=1) == uns
+    assert library(sequences=1, rows=1, heads=65, max_pages=2 ** 24, group=1) == uns
+    assert library(sequences=1, rows=0, max_new=0, heads=63, max_pages=2 ** 24, group=1) == (fa.FP4ATTN_OK,) * 2
