@@ -1040,6 +1040,17 @@ size_t attn_workspace(int D, int B, int heads, int max_pages, long long cols) {
   return plan_bytes() + static_cast<size_t>(attn_ctas(D, tile_nt(D, cols))) * kWarps * 2 * (8 * tile_nt(D, cols)) * (D + 2) * sizeof(float);
 }
 
+// Limits of the sizes, which are positive.
+int check_sizes(int heads, int B, int max_pages, int group, int max_new) {
+  if (B > kMaxKvBatch || max_pages > kMaxSlots / kPage) return FP4ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(heads) * group > 65535) return FP4ATTN_ERR_UNSUPPORTED;
+  const long long cols = static_cast<long long>(max_new) * group;
+  if (cols > (1ll << 24)) return FP4ATTN_ERR_UNSUPPORTED;
+  // units of all tiles must stay within 32 bits, rounded up to whole runs too
+  if (static_cast<long long>(B) * heads * ((cols + 7) / 8) >= (1ll << 30) / max_pages) return FP4ATTN_ERR_UNSUPPORTED;
+  return FP4ATTN_OK;
+}
+
 // Checks shared by attention and weights.
 int check_attn(const fp4attn_kv_cache_t* c, const fp4attn_kv_batch_t* b, const void* q, long long q_row,
                long long q_head, int group, int max_new, float scale, float cap, int window) {
@@ -1052,12 +1063,7 @@ int check_attn(const fp4attn_kv_cache_t* c, const fp4attn_kv_batch_t* b, const v
   const float up = scale * ldexpf(1.0f, c->k_exp);  // what the kernels multiply by
   if (!std::isnormal(up) || (cap > 0.0f && !std::isfinite(up / cap))) return FP4ATTN_ERR_INVALID_ARG;
   if (b->T > 0 && (!q || !aligned16(q) || ((q_row | q_head) & 7))) return FP4ATTN_ERR_INVALID_ARG;
-  if (static_cast<long long>(c->heads) * group > 65535) return FP4ATTN_ERR_UNSUPPORTED;
-  // units of all tiles must stay within 32 bits, rounded up to whole runs too
-  const long long cols = static_cast<long long>(max_new) * group;
-  if (cols > (1ll << 24)) return FP4ATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>(b->B) * c->heads * ((cols + 7) / 8) >= (1ll << 30) / b->max_pages) return FP4ATTN_ERR_UNSUPPORTED;
-  return FP4ATTN_OK;
+  return check_sizes(c->heads, b->B, b->max_pages, group, max_new);
 }
 
 }  // namespace
@@ -1069,6 +1075,8 @@ extern "C" int fp4attn_kv_attention_workspace_bytes(int heads, int D, int B, int
                                                     size_t* bytes) {
   if (heads <= 0 || B <= 0 || max_pages <= 0 || group <= 0 || max_new < 0 || !bytes) return FP4ATTN_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return FP4ATTN_ERR_UNSUPPORTED;
+  const int st = check_sizes(heads, B, max_pages, group, max_new);
+  if (st != FP4ATTN_OK) return st;
   *bytes = attn_workspace(D, B, heads, max_pages, static_cast<long long>(group) * max_new);
   return FP4ATTN_OK;
 }

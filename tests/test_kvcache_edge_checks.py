@@ -46,3 +46,14 @@ def test_work_that_32_bits_do_not_count(fa, library):
     assert library(sequences=337, rows=337, heads=6223, max_pages=1024, group=1) == uns
     assert library(sequences=1, rows=1, heads=65, max_pages=2 ** 24, group=1) == uns
     assert library(sequences=1, rows=0, max_new=0, heads=63, max_pages=2 ** 24, group=1) == (fa.FP4ATTN_OK,) * 2
+
+
+def test_workspace_of_sizes_that_the_call_refuses(fa):
+    from blackwell_nvfp4_quantize_gb300 import kvcache as kv
+
+    n = ctypes.c_size_t()
+    f = kv._L().fp4attn_kv_attention_workspace_bytes
+    big = 2 ** 31 - 1
+    for heads, seqs, pages, group, new in ((H, 2049, 8, 1, 1), (H, 4, 2 ** 24 + 1, 1, 1), (70000, 4, 8, 1, 1),
+                                           (40000, 4, 8, 2, 1), (big, big, big, 1, 64), (H, 4, 8, 1, 2 ** 24 + 1)):
+        assert f(heads, 128, seqs, pages, group, new, ctypes.byref(n)) == fa.FP4ATTN_ERR_UNSUPPORTED, (heads, seqs, pages)
