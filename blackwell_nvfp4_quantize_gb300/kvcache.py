@@ -162,6 +162,10 @@ def _check_rows(t, name, heads, D, dev, T):
     if t.get_device() != dev:
         raise _elsewhere(t, name, dev)
     r, s, e = t.stride()
+    if n == 1:  # a stride that addresses nothing may be anything
+        r = 0
+    if h == 1:
+        s = 0
     at = t.data_ptr()
     if (e != 1 or (r | s) & 7 or at & 15) and n:
         raise ValueError("%s needs contiguous channels, strides that are multiples of 8 and a 16-byte aligned start" % name)

@@ -278,3 +278,18 @@ def test_rows_before_the_first_sequence_stay(fa, n):
         ok(fa)
         assert torch.equal(o[11:17], want[0]) and torch.equal(lse[11:17], want[1])
         assert torch.all(o[:11] == 3.0) and torch.all(o[17:] == 3.0) and torch.all(lse[:11] == 5.0)
+
+
+def test_one_row_of_one_head_with_any_strides(fa):
+    s = Setup(fa, [70], [1], H=1, D=64, seed=6)
+    s.append_all()
+    ok(fa)
+    pages = s.cache.pages.clone()
+    odd = [torch.empty_strided((1, 1, 64), (67, 129, 1), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for x, y in zip(odd, (s.k[0], s.v[0])):
+        x.copy_(y[69:70])
+    fa.kv_append(odd[0], odd[1], s.cache, s.d_table, s.d_lens)  # the same row again
+    a = fa.kv_attention(odd[0], s.cache, s.d_table, s.d_lens)
+    b = fa.kv_attention(odd[0].contiguous(), s.cache, s.d_table, s.d_lens)
+    ok(fa)
+    assert torch.equal(s.cache.pages, pages) and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])

@@ -57,3 +57,20 @@ def test_workspace_of_sizes_that_the_call_refuses(fa):
     for heads, seqs, pages, group, new in ((H, 2049, 8, 1, 1), (H, 4, 2 ** 24 + 1, 1, 1), (70000, 4, 8, 1, 1),
                                            (40000, 4, 8, 2, 1), (big, big, big, 1, 64), (H, 4, 8, 1, 2 ** 24 + 1)):
         assert f(heads, 128, seqs, pages, group, new, ctypes.byref(n)) == fa.FP4ATTN_ERR_UNSUPPORTED, (heads, seqs, pages)
+
+
+@pytest.mark.parametrize("name", ["append", "attention", "accumulate"])
+def test_strides_of_a_dimension_of_one_do_not_matter(fa, name):
+    """A single row, or a single head, of a wider tensor: what its stride says addresses nothing."""
+    f, a = calls(fa)[name]
+    rows = [x for x in ("k", "v", "q") if x in a]
+    one = dict(cache=cache(fa, pages=torch.zeros((P, 1, 72 * D), dtype=torch.uint8)), table=i32(1, M), lens=i32(1))
+    if name == "accumulate":
+        one.update(lse=torch.zeros((1, 1)), weights=torch.zeros((1, 1, 64 * M)))
+    x = torch.empty_strided((1, 1, D), (D + 3, 2 * D + 1, 1), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):  # the last check: everything else is in order
+        f(**{**a, **one, **{n: x for n in rows}})
+    x = torch.empty_strided((3, 1, D), (D + 3, D, 1), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="multiples of 8"):
+        f(**{**a, **one, **{n: x for n in rows}, **dict(table=i32(3, M), lens=i32(3)),
+             **(dict(lse=torch.zeros((3, 1)), weights=torch.zeros((3, 1, 64 * M))) if name == "accumulate" else {})})
