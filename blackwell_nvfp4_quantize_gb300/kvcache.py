@@ -80,8 +80,15 @@ class KVCache:
         return self.pages.shape[1]
 
 
+def _in_32_bits(*numbers):
+    """ctypes cuts a number to its low bits without a word."""
+    if not all(-2 ** 31 <= x < 2 ** 31 for x in numbers):
+        raise ValueError("%s: sizes must be numbers that 32 bits hold" % (numbers,))
+
+
 def kv_page_bytes(heads: int, D: int) -> int:
     """Bytes of one page (64 tokens) of all KV heads."""
+    _in_32_bits(heads, D)
     n = ctypes.c_size_t()
     _check(_L().fp4attn_kv_page_bytes(heads, D, ctypes.byref(n)), "fp4attn_kv_page_bytes")
     return n.value
@@ -98,6 +105,7 @@ def empty_kv_cache(num_pages: int, heads: int, D: int, device, k_exp: int = 0, v
 # microseconds: each looks at an attribute once and builds no message before it
 # is needed.  Devices are compared by index (-1: the CPU).
 
+_MOST = 2 ** 31 - 1  # of a number for the library; more than it accepts of any
 _Tensor, _i32, _f32, _bf16, _u8 = torch.Tensor, torch.int32, torch.float32, torch.bfloat16, torch.uint8
 # (not there in a torch without CUDA, where every call stops at its checks)
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
@@ -143,8 +151,12 @@ def _geometry(cache, table, lens, cu, T, rows=True):
     elif rows and (B == 0 or T % B):
         raise ValueError("%d rows do not divide among %d sequences: cu is needed" % (T, B))
     num_pages, heads, _ = shape
-    return (_pack_cache(pages.data_ptr(), num_pages, heads, D, cache.k_exp, cache.v_exp),
-            _pack_batch(table.data_ptr(), lens.data_ptr(), at, B, M, T), dev, heads, D, B, M)
+    try:
+        return (_pack_cache(pages.data_ptr(), num_pages, heads, D, cache.k_exp, cache.v_exp),
+                _pack_batch(table.data_ptr(), lens.data_ptr(), at, B, M, T), dev, heads, D, B, M)
+    except struct.error:
+        raise ValueError("exponents %r, %r and sizes %s must be whole numbers that 32 bits hold"
+                         % (cache.k_exp, cache.v_exp, (num_pages, heads, B, M, T))) from None
 
 
 def _rows(t):
@@ -266,6 +278,7 @@ def _workspace_of(dev, *sizes):
 
 def kv_attention_workspace_bytes(heads: int, D: int, B: int, max_pages: int, group: int, max_new: int) -> int:
     """Bytes of kv_attention's workspace for a table [B, max_pages] (0: none needed)."""
+    _in_32_bits(heads, D, B, max_pages, group, max_new)
     n = ctypes.c_size_t()
     _check(_L().fp4attn_kv_attention_workspace_bytes(heads, D, B, max_pages, group, max_new, ctypes.byref(n)),
            "fp4attn_kv_attention_workspace_bytes")
@@ -344,7 +357,7 @@ def kv_accumulate(q: torch.Tensor, lse: torch.Tensor, weights: torch.Tensor, cac
     _check_out(weights, "weights", _f32, (B, heads, W), dev)
     handle, _ = _stream_of(stream, dev)
     _launch(dev, "fp4attn_kv_accumulate", c, b, at, r, s, group, max_new, scale, softcap, window, slope_at,
-            lse.data_ptr(), weights.data_ptr(), W, decay, handle)
+            lse.data_ptr(), weights.data_ptr(), min(W, _MOST), decay, handle)
     return weights
 
 
@@ -380,6 +393,6 @@ def kv_evict(cache: KVCache, weights: torch.Tensor, table: torch.Tensor, lens: t
         new_lens = _new((B,), _i32, dev, side)
     if new_weights is None:
         new_weights = _new(weights.shape, _f32, dev, side)
-    _launch(dev, "fp4attn_kv_evict", c, b, weights.data_ptr(), W, new_table.data_ptr(), ns[1], keep, sinks, recent,
-            kept.data_ptr(), new_lens.data_ptr(), new_weights.data_ptr(), handle)
+    _launch(dev, "fp4attn_kv_evict", c, b, weights.data_ptr(), min(W, _MOST), new_table.data_ptr(), min(ns[1], _MOST),
+            keep, sinks, recent, kept.data_ptr(), new_lens.data_ptr(), new_weights.data_ptr(), handle)
     return kept, new_lens, new_weights

@@ -293,3 +293,19 @@ def test_one_row_of_one_head_with_any_strides(fa):
     b = fa.kv_attention(odd[0].contiguous(), s.cache, s.d_table, s.d_lens)
     ok(fa)
     assert torch.equal(s.cache.pages, pages) and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_weights_wider_than_32_bits_count(fa):
+    """2^32 + 64 slots (17 GB) are refused like any number above 2^30."""
+    s = Setup(fa, [100], [1], H=1, D=64, seed=6)
+    s.append_all()
+    q = s.queries(1).cuda()
+    _, lse = fa.kv_attention(q, s.cache, s.d_table, s.d_lens)
+    w = torch.empty((1, 1, 2 ** 32 + 64), device="cuda")
+    nt = torch.from_numpy(s.spare[:1].reshape(1, 1).copy()).cuda()
+    for call in (lambda: fa.kv_accumulate(q, lse, w, s.cache, s.d_table, s.d_lens),
+                 lambda: fa.kv_evict(s.cache, w, s.d_table, s.d_lens, nt, 60)):
+        with pytest.raises(fa.Fp4AttnError) as e:
+            call()
+        assert e.value.status == fa.FP4ATTN_ERR_UNSUPPORTED
+    ok(fa)

@@ -74,3 +74,19 @@ def test_strides_of_a_dimension_of_one_do_not_matter(fa, name):
     with pytest.raises(ValueError, match="multiples of 8"):
         f(**{**a, **one, **{n: x for n in rows}, **dict(table=i32(3, M), lens=i32(3)),
              **(dict(lse=torch.zeros((3, 1)), weights=torch.zeros((3, 1, 64 * M))) if name == "accumulate" else {})})
+
+
+def test_numbers_that_32_bits_do_not_hold(fa):
+    """They are refused, not cut to their low bits."""
+    for f, a in calls(fa).values():
+        for bad in (cache(fa, k_exp=2 ** 40), cache(fa, v_exp=1.5), cache(fa, k_exp=None)):
+            with pytest.raises(ValueError, match="32 bits"):
+                f(**{**a, "cache": bad})
+    f, a = calls(fa)["read"]
+    with pytest.raises(ValueError, match="32 bits"):
+        f(**{**a, "total": B * 2 ** 32})
+    for call in (lambda: fa.kv_page_bytes(2 ** 32 + 1, 64), lambda: fa.kv_page_bytes(1, 2 ** 32 + 64),
+                 lambda: fa.kv_attention_workspace_bytes(H, D, 2 ** 32 + 1, M, 1, 1),
+                 lambda: fa.kv_attention_workspace_bytes(H, D, 1, M, 1, 2 ** 32 + 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
