@@ -18,15 +18,18 @@ DeviceStatus* device_status_ptr() {
   std::lock_guard<std::mutex> lock(g_mu);
   if (!g_status[dev]) {
     // The first call may fall into a stream capture of the caller's: neither
-    // the allocation nor the set-up copy is part of it.
+    // the allocation nor the set-up is part of it, and the set-up has a stream of
+    // its own, as the legacy one may not be used while a stream that waits for it
+    // is captured.
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
     void* p = nullptr;
-    bool ok = cudaMalloc(&p, 256) == cudaSuccess;
-    if (ok && cudaMemset(p, 0, 256) != cudaSuccess) {
-      cudaFree(p);
-      ok = false;
-    }
+    cudaStream_t s = nullptr;
+    bool ok = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) == cudaSuccess;
+    ok = ok && cudaMalloc(&p, 256) == cudaSuccess;
+    ok = ok && cudaMemsetAsync(p, 0, 256, s) == cudaSuccess && cudaStreamSynchronize(s) == cudaSuccess;
+    if (s) cudaStreamDestroy(s);
+    if (!ok && p) cudaFree(p);
     cudaThreadExchangeStreamCaptureMode(&mode);
     if (!ok) return nullptr;
     g_status[dev] = static_cast<DeviceStatus*>(p);

@@ -309,3 +309,37 @@ def test_weights_wider_than_32_bits_count(fa):
             call()
         assert e.value.status == fa.FP4ATTN_ERR_UNSUPPORTED
     ok(fa)
+
+
+def test_first_call_of_a_process_in_a_capture_of_a_blocking_stream():
+    """While a stream that waits for the legacy one is being captured, nothing may use the legacy stream: the set-up of
+    the library's status word does not."""
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import ctypes, re
+import torch, blackwell_nvfp4_quantize_gb300 as fa
+i32 = dict(dtype=torch.int32, device='cuda')
+c = fa.empty_kv_cache(4, 2, 64, 'cuda')
+k = torch.ones((1, 2, 64), dtype=torch.bfloat16, device='cuda')
+table, lens = torch.tensor([[3]], **i32), torch.tensor([1], **i32)
+torch.cuda.synchronize()
+so = {l.split()[-1] for l in open('/proc/self/maps') if re.search(r'libcudart\\.so', l)}
+rt = ctypes.CDLL(so.pop())
+st, graph, run = ctypes.c_void_p(), ctypes.c_void_p(), ctypes.c_void_p()
+assert rt.cudaStreamCreate(ctypes.byref(st)) == 0
+assert rt.cudaStreamBeginCapture(st, 0) == 0
+fa.kv_append(k, k, c, table, lens, stream=st.value)
+assert rt.cudaStreamEndCapture(st, ctypes.byref(graph)) == 0
+assert rt.cudaGraphInstantiate(ctypes.byref(run), graph, ctypes.c_ulonglong(0)) == 0
+assert rt.cudaGraphLaunch(run, st) == 0 and rt.cudaStreamSynchronize(st) == 0
+a, b = fa.kv_read(c, table, lens, 1)
+torch.cuda.synchronize()
+assert fa.device_status() == 0 and torch.equal(b, a) and torch.all((a - 1).abs() < 0.1), a
+print('done')
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "done" in r.stdout, r.stdout + r.stderr
