@@ -447,19 +447,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
       const int at_lo = __reduce_min_sync(0xFFFFFFFFu, at), at_hi = __reduce_max_sync(0xFFFFFFFFu, at);
       float m = -INFINITY, l = 0.0f;
       uint32_t pages = 3u;  // of the block at hand: bit i, page i counts
+      // (Before its scores come, where that costs nothing, but for the first block:
+      // a tile that had no rows in the segments before may be here while the
+      // operands are many blocks behind, and the barrier's phase an older one.
+      // Within a segment it is this block's, for the one before has been done.)
+      auto ask = [&]() {
+        ok = mbar_wait(seen_full + ks % kSeen, ks / kSeen & 1, abort_flag, p.g.status, 83);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (ok) pages = seen[ks % kSeen];
+        return ok;
+      };
       // page by page: while this warpgroup works on one page's scores, the tensor
       // core takes the other's P and refills its S
       for (int i = 0; i < 2 * nblk; ++i) {
         const int pg = i & 1;
-        if (pg == 0) {  // (long there when the scores come, and here it costs nothing)
-          ok = mbar_wait(seen_full + ks % kSeen, ks / kSeen & 1, abort_flag, p.g.status, 83);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          pages = seen[ks % kSeen];
-        }
+        if (pg == 0 && i > 0 && !ask()) break;
         ok = mbar_wait(s_full + 2 * t + pg, kc & 1, abort_flag, p.g.status, 72);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
+        if (i == 0 && !ask()) break;
         tc_fence_after();
         const uint32_t tp = ts + kPage * pg;
         const int slot0 = (x.first + (u + (i >> 1) - x.begin)) * kBlockKeys + kPage * pg;

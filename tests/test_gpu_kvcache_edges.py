@@ -343,3 +343,41 @@ print('done')
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "done" in r.stdout, r.stdout + r.stderr
+
+
+def plain_attention(fa, s, q, G, cap=0.0, window=0):
+    """(O, LSE) in float64 on the GPU, of the values that the cache holds."""
+    o = torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+    lse = torch.full(q.shape[:2], -float("inf"), dtype=torch.float64, device="cuda")
+    for b, (L, n) in enumerate(zip(s.lens, s.news)):
+        one = (s.cache, s.d_table[b:b + 1].contiguous(), s.d_lens[b:b + 1].contiguous())
+        k, v = (x.double().repeat_interleave(G, 1) for x in fa.kv_read(*one, L))
+        rows = slice(int(s.cu[b]), int(s.cu[b + 1]))
+        x = torch.einsum("nhd,lhd->hnl", q[rows].double(), k) * s.D ** -0.5
+        if cap:
+            x = cap * torch.tanh(x / cap)
+        dist = torch.arange(L - n, L, device="cuda")[:, None] - torch.arange(L, device="cuda")
+        x.masked_fill_((dist < 0) | (dist >= window if window else dist < 0), -float("inf"))
+        lse[rows] = torch.logsumexp(x, -1).T
+        o[rows] = torch.einsum("hnl,lhd->nhd", torch.softmax(x, -1), v)
+    return o, lse
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window,cap", [(1024, 50.0), (0, 0.0)])
+def test_prompts_from_cold_memory(fa, D, window, cap):
+    """Problems of two tiles between others of one, so that a tile's warps come to a problem long before its operands,
+    which memory delays further; other bytes lie in shared memory at each start."""
+    lens, news = [2100, 1500, 1019, 1300], [261, 257, 130, 130]
+    s = Setup(fa, lens, news, H=4, D=D, seed=11)
+    s.append_all()
+    q = s.queries(4).cuda()
+    ro, rl = plain_attention(fa, s, q, 4, cap, window)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for turn in range(6):
+        flush.fill_(turn)
+        o, lse = rows_alone(fa, s, q, softcap=cap, window=window)
+        ok(fa)
+        # bf16 and fp16 roundings (2^-8 |O| + 2^-11 |V|), and the scores' errors (below 2^-14 here)
+        assert torch.all((o.double() - ro).abs() <= 2.0 ** -8 * ro.abs() + (2.0 ** -11 + 2.0 ** -13) * 6), turn
+        assert torch.all((lse.double() - rl).abs() <= 2.0 ** -14), turn
