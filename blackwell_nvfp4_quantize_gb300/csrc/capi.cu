@@ -57,7 +57,7 @@ extern "C" const char* fp4attn_status_string(int status) {
   switch (status) {
     case FP4ATTN_OK: return "ok";
     case FP4ATTN_ERR_INVALID_ARG: return "invalid argument (null or misaligned pointer, bad size or scale)";
-    case FP4ATTN_ERR_UNSUPPORTED: return "unsupported shape (D must be 64 or 128; B*H <= 65535; B*H*N < 2^31)";
+    case FP4ATTN_ERR_UNSUPPORTED: return "unsupported shape (D must be 64 or 128; B*H <= 65535; B*H*N < 2^31; key/value cache: at most 2048 sequences, 2^28 rows, 65535 heads)";
     case FP4ATTN_ERR_CUDA: return "CUDA runtime error";
     case FP4ATTN_ERR_TIMEOUT: return "a bounded device-side wait timed out; outputs are incomplete";
     case FP4ATTN_ERR_BAD_INDEX: return "a kernel skipped a page, length or row offset out of range; outputs are incomplete";

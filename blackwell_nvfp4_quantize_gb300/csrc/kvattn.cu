@@ -967,8 +967,14 @@ int tile_nt(int D, long long cols) {
 
 // Columns beyond which the kernel for prompts takes over, whose time hardly
 // depends on them up to 512: three tiles for D = 128, two for D = 64.  Measured
-// at 16 sequences of 8192 tokens, 8 KV heads (us): D = 128, one tile 55, two 87,
-// the prompt kernel 195 to 205; D = 64, one tile 56, two 89, the prompt kernel 155.
+// with 8 KV heads (us; this kernel, beyond the limits also the one for prompts):
+//   sequences x tokens  D = 128: 48 columns, 64, 80, 96     D = 64: 64 columns, 80, 96, 128
+//   1 x 8192     19  19 / 31    28 / 32    28 / 32           19   20 / 26    20 / 27    20 / 27
+//   16 x 8192   123  157 / 193  193 / 198  227 / 201         91  126 / 157  129 / 159  160 / 161
+//   64 x 4096   252  329 / 389  409 / 398  489 / 402        172  257 / 322  265 / 324  345 / 329
+//   64 x 512     92  108 / 86   150 / 86   180 / 88          65  103 / 71   106 / 72   117 / 73
+// Many short sequences cross over at the limits, long ones one or two tiles
+// later; the lengths, which would tell them apart, are not known on the host.
 bool is_prompt(int D, long long cols) { return cols > (D == 128 ? 48 : 64); }
 long long tiles_of(int D, long long cols) {
   const int width = 8 * tile_nt(D, cols);

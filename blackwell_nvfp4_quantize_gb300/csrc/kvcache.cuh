@@ -180,8 +180,8 @@ cudaError_t allow_smem(int bytes) {
 // Launches.  A kernel that starts with chain_start() may come up while the one
 // before it in the stream runs, if that one has let it (chain_next), and touches
 // no memory before all that came before is done (chain_wait).  Saves a few
-// tenths of a microsecond per kernel, 6 where a kernel prepares before it waits
-// (the join of a prompt's partial results).
+// tenths of a microsecond per kernel, more where a kernel prepares before it
+// waits (the join behind the attention of few queries).
 __device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void chain_start() {

@@ -68,8 +68,9 @@ constexpr int kSeen = 8;    // blocks whose pages the rows' warps may still ask 
 constexpr int kBlockKeys = 128;
 constexpr int kWarpDq = 8, kWarpMma = 12;
 // Four warpgroups: two for the rows, one for the operands, one whose first
-// warp issues the MMAs.  The rows' threads hold 128 scores each, so registers
-// go from the others to them: 2 x 176 + 96 + 64 = 4 x 128.
+// warp issues the MMAs.  The rows' threads hold 64 scores each, and what turns
+// them into P, so registers go from the others to them: 2 x 176 + 96 + 64 = 4 x
+// 128.  (One register at most is spilled.)
 constexpr int kPromptThreads = 512;
 constexpr int kRegsRows = 176, kRegsOperands = 96, kRegsMma = 64;
 static_assert(2 * kRegsRows + kRegsOperands + kRegsMma == 4 * 128, "registers of the launch");

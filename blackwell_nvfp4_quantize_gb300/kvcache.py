@@ -366,7 +366,10 @@ def kv_evict(cache: KVCache, weights: torch.Tensor, table: torch.Tensor, lens: t
              new_lens: torch.Tensor | None = None, new_weights: torch.Tensor | None = None, stream=None):
     """fp4attn_kv_evict: keeps, of every sequence and KV head, the first `sinks` tokens, the last `recent` and the
     heaviest others, `keep` in all, and copies them to the pages of new_table (pages that table does not list).
-    (kept int32 [B, heads, keep], new_lens int32 [B], new_weights like weights)."""
+    (kept int32 [B, heads, keep], new_lens int32 [B], new_weights like weights): from here on these and new_table
+    (with more pages behind, for what is to come) take the place of lens, weights and table.  The kept tokens have
+    new slots, 0 .. new_lens - 1, and windows and slopes then count slots, not the tokens that were between; kept
+    says which they were."""
     c, b, dev, heads, _, B, _ = _geometry(cache, table, lens, None, 0, rows=False)
     ns = _index_shape(new_table, "new_table", dev)
     if len(ns) != 2 or ns[0] != B:

@@ -75,7 +75,7 @@ extern "C" {
 enum {
     FP4ATTN_OK = 0,
     FP4ATTN_ERR_INVALID_ARG = 1, /* null or misaligned pointer, bad size, non-finite scale */
-    FP4ATTN_ERR_UNSUPPORTED = 2, /* D not in {64, 128}, sizes beyond the supported range */
+    FP4ATTN_ERR_UNSUPPORTED = 2, /* D not in {64, 128}, sizes beyond the call's range */
     FP4ATTN_ERR_CUDA = 3,        /* a CUDA runtime call or kernel launch failed */
     FP4ATTN_ERR_TIMEOUT = 4,     /* a bounded device-side wait gave up (see fp4attn_device_status) */
     FP4ATTN_ERR_BAD_INDEX = 5    /* a cache call skipped an index out of range (see fp4attn_device_status) */
@@ -445,7 +445,8 @@ int fp4attn_fwd_host_batch(int nsteps, const void *const *q_h, const void *const
  * row j % 64.  Every call takes lens[b], the number of tokens of the sequence
  * AFTER the new ones of the call have been added: its n new tokens have the
  * slots lens[b] - n .. lens[b] - 1.  table, lens and cu are device memory, so
- * that a captured graph can be replayed for longer sequences.  A page outside
+ * that a captured graph can be replayed for longer sequences; they stay as they
+ * are while a call that reads them runs.  A page outside
  * [0, num_pages), a length outside [0, 64 max_pages], rows outside [0, T) or a
  * sequence with more new tokens than max_new is skipped (a page counts as
  * unseen, a sequence's rows stay as they were), where row offsets descend some
@@ -455,7 +456,12 @@ int fp4attn_fwd_host_batch(int nsteps, const void *const *q_h, const void *const
  * weight) read those of pages before the windows of all its queries, or let
  * what else lies outside their reach count.  Sequences may share pages of
  * tokens that are already written; a page that receives new tokens belongs to
- * one.  At most 2048 sequences, 2^24 pages per sequence and 2^28 rows per call. */
+ * one.  At most 2048 sequences, 2^24 pages per sequence, 2^28 rows and 65535
+ * heads per call, 2^24 queries per sequence and KV head, and 2^30 pages over all
+ * sequences, KV heads and eights of those queries.
+ * append stores finite values; where pages come from elsewhere, a token with a
+ * NaN scale that some query of a call sees may make rows that do not see it NaN
+ * too. */
 typedef struct {
     uint8_t *pages; /* [num_pages, heads, 72 D], 16-byte aligned */
     int num_pages;
@@ -530,8 +536,11 @@ int fp4attn_kv_accumulate(const fp4attn_kv_cache_t *cache, const fp4attn_kv_batc
  * order, are copied bit for bit to the pages of new_table ([B, new_max_pages],
  * pages that no table row of the call lists); kept: int32 [B, heads, keep], their
  * old slots, -1 past the last; new_lens [B] = min(lens, keep); new_weights
- * [B, heads, weights_stride]: their weights, 0 past the last.  batch->cu and T are not used.
- * Outputs must not be inputs.  Two kernels. */
+ * [B, heads, weights_stride]: their weights (a zero as +0), 0 past the last.
+ * The kept tokens' slots are 0 .. new_lens - 1 from here on: windows and slopes
+ * of later calls count these.  A sequence whose length is out of range (or above
+ * weights_stride) comes out empty.  batch->cu and T are not used.  Outputs must
+ * not be inputs, nor new_table's pages listed twice.  Two kernels. */
 int fp4attn_kv_evict(const fp4attn_kv_cache_t *cache, const fp4attn_kv_batch_t *batch, const float *weights,
                      int weights_stride, const int32_t *new_table, int new_max_pages, int keep, int sinks, int recent,
                      int32_t *kept, int32_t *new_lens, float *new_weights, void *stream);
