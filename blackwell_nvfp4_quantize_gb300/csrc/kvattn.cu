@@ -37,10 +37,11 @@
 // results do not depend on timing.
 //
 // Measured (8 KV heads, D = 128; of 6.8 TB/s that a copy reaches): 64 sequences
-// to 8192 tokens, 8 query heads per KV head, 62 us and 7 for the join, 4.7 TB/s
-// (ALU pipe 50%, issue slots 55%, 12 warps per SM); 3 sequences to 131072 tokens
-// 74 us and 8, 5.6 TB/s; one sequence of 4096 8.4 us.  Gathered weight, 32
-// sequences to 16384 tokens: 36 us, 4.4 TB/s.
+// to 8192 tokens, 8 query heads per KV head, 63 us and 8 for the join, 4.7 TB/s
+// (DRAM 59%, ALU pipe 50%, issue slots 55%; in 45% of the cycles none of a
+// scheduler's 2.7 warps can issue); 3 sequences to 131072 tokens 74 us and 9, 5.6
+// TB/s; one sequence of 4096 8.2 us.  Gathered weight, 32 sequences to 16384
+// tokens: 36 us, 4.4 TB/s (DRAM 51%, ALU pipe 39%, issue slots 51%).
 #include <type_traits>
 
 #include "kvattn.cuh"

@@ -31,7 +31,7 @@
 //              about 1300 cycles, and these have the time.
 // K and V of a block are handed over together: the hand-offs (a proxy fence and a
 // release, which wait for the loads on their way) are what the operands' warps
-// have least time for (prompt_chunk 955 us, with one for each 1000).
+// have least time for (955 us where one for each took 1000).
 // S, P and the products go page by page (64 tokens): a warpgroup alternates
 // between its tile's two pages, and while it works on one the tensor core takes
 // the other's P, refills its S, and serves the other tile.  TMEM: S 2 x 128 columns, O 2 x D.
@@ -39,12 +39,12 @@
 // are written, so that its first scores are made meanwhile.
 //
 // Measured (of 1895 TFLOP/s, a large library product of bf16): D = 128, 2
-// sequences of 16384 tokens, 2048 of them new, 40 query heads over 8: 946 us,
-// 1360 TFLOP/s, 72%.  What bounds it is the chain S -> P -> products of a page,
-// whose hand-offs the tensor core waits for 40% of the time; the
-// exponentials' unit is busy 30%, the ALUs 28%.  D = 64, 7 prompts of 3333 rows in
-// all, 16 query heads over 4, window 1024, capped: 66 us (without the cap 50), of
-// which 32 remain with a window of one token: start, join, and for each of the 2
+// sequences of 16384 tokens, 2048 of them new, 40 query heads over 8: 964 us,
+// 1335 TFLOP/s, 70%.  The tensor core waits 40% of the time, for the hand-offs of
+// a page's chain S -> P -> products; no unit is full (exponentials 30%, ALUs 29%,
+// issue slots 46%).  D = 64, 7 prompts of 3333 rows in all, 16 query heads over 4,
+// window 1024, capped: 72 us (without the cap 54), of which 31 remain with a
+// window of one token: start, join, and for each of the 2
 // or 3 problems of a pair its queries, first scores and results.
 //
 // P is held as 2^(15 - slack) p against a reference maximum that may lag by
@@ -54,7 +54,7 @@
 // before they are rounded.  L tokens together then lose L 2^(slack - 40) of the
 // largest |V| at most: the slack is 12 up to 2^17 tokens, where that is 2^-11
 // (a quarter of bf16's rounding), and one less with every further doubling, down
-// to 1.  (A slack of 8 for all costs 3%: prompt_chunk 984 us, of 4 992.)
+// to 1.  (For all lengths alike, a slack of 8 took 984 us in place of 951, of 4 992.)
 #include <type_traits>
 
 #include "kvattn.cuh"
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
     struct Block {
       int page[2];  // table entries, where looks() says so
       int first;    // number of the first page
-      int lo, L;    // the problem's queries see slots in [lo, L) alone (one comparison each below: 962 us, two 977)
+      int lo, L;    // the problem's queries see slots in [lo, L) alone (one comparison below; with two 977 us, not 962)
       int h;
     };
     // Whether page i of a block holds a token that some query sees: others are

@@ -166,8 +166,7 @@ def test_memory_of_a_call_on_another_stream(fa, name, columns, handle):
 
 @pytest.mark.parametrize("D", [64, 128])
 def test_prompts_write_every_row(fa, D):
-    """No row of a sequence is left as it was, whatever the batch (the size of the largest moves the kernel's shared
-    memory about)."""
+    """No row of a sequence is left as it was, whatever the batch (the kernel's shared memory grows with it)."""
     for B in (1, 3, 130, 2048):
         news = [70 if b % 700 == 0 else 1 for b in range(B)]
         s = Setup(fa, news, news, H=1, D=D, seed=B)
