@@ -25,10 +25,10 @@
 //   warp 12    of the first CTA issues tcgen05.mma (kind::f16): S = Q K^T from
 //              shared memory, O += P V with P as fp16 in TMEM, over the columns
 //              S came in.
-//   warps 13, 14 of the second CTA pass on to it that operands and queries are
-//              in place there: what one CTA wrote to its shared memory for an MMA
-//              of the other needs a release at cluster scope, which costs the warp
-//              about 1300 cycles, and these have the time.
+//   warp 13    of the second CTA passes on to it that operands are in place
+//              there: what one CTA wrote to its shared memory for an MMA of the
+//              other needs a release at cluster scope, which costs the warp about
+//              1300 cycles, and this one has the time.
 // K and V of a block are handed over together: the hand-offs (a proxy fence and a
 // release, which wait for the loads on their way) are what the operands' warps
 // have least time for (955 us where one for each took 1000).
@@ -70,7 +70,7 @@ constexpr int kWarpDq = 8, kWarpMma = 12;
 // Four warpgroups: two for the rows, one for the operands, one whose first
 // warp issues the MMAs.  The rows' threads hold 64 scores each, and what turns
 // them into P, so registers go from the others to them: 2 x 176 + 96 + 64 = 4 x
-// 128.  (One register at most is spilled.)
+// 128.  (32 bytes a thread are spilled.)
 constexpr int kPromptThreads = 512;
 constexpr int kRegsRows = 176, kRegsOperands = 96, kRegsMma = 64;
 static_assert(2 * kRegsRows + kRegsOperands + kRegsMma == 4 * 128, "registers of the launch");
@@ -88,7 +88,7 @@ struct PromptSmem {
   static constexpr int kK = kQ + 2 * kQTile;
   static constexpr int kV = kK + kStages * kKTile;
   static constexpr int kBars = kV + kStages * kVTile;
-  static constexpr int kNumBars = 2 + 3 * kStages + 4 + 4 + 4 + 1 + 2 + kStages + kSeen;
+  static constexpr int kNumBars = 2 + 3 * kStages + 4 + 4 + 4 + 1 + kStages + kSeen;
   static constexpr int kMisc = kBars + kNumBars * 8;
   static constexpr int kPrefix = kMisc + 128;
   static int bytes(int B) {
@@ -119,21 +119,23 @@ constexpr uint32_t kDescHigh = 64u | (1u << 14) | (2u << 29);
 
 // M = 256 over the CTA pair: A and D rows 128 in each CTA (the same offsets), B
 // rows N / 2 in each.  The whole warp comes here with operands that are
-// constants; one lane, elected once per batch, issues the MMAs of a batch and
-// the commit that reports them to both CTAs.
-// S of tile T, page PG of stage S (32 key rows of the page in each CTA)
-// (base: shared memory's address / 16, the same in both CTAs)
-template <int D, int T, int PG, int S>
-__device__ __forceinline__ void issue_qk(uint32_t base, uint32_t s_full) {
+// the same in every lane; one, elected once per batch, issues the MMAs of a batch
+// and the commit that reports them to both CTAs.  (Stages as template arguments
+// made four copies of the loop over the blocks, and 964 us of 928: the roles'
+// instructions share one cache.)
+// S of tile T, page PG (32 key rows of the page in each CTA).  q: of the queries'
+// tiles in shared memory, k: of the stage, addresses / 16, the same in both CTAs
+template <int D, int T, int PG>
+__device__ __forceinline__ void issue_qk(uint32_t q, uint32_t k, uint32_t s_full) {
   using L_ = PromptSmem<D>;
   constexpr uint32_t d = kColS + 128 * T + kPage * PG, id = idesc_f16(256, kPage);
-  constexpr uint32_t a = desc_low(L_::kQ + T * L_::kQTile), b = desc_low(L_::kK + S * L_::kKTile + PG * (32 * 128));
+  constexpr uint32_t a = desc_low(T * L_::kQTile), b = desc_low(PG * (32 * 128));
   // to the next 64 channels
   constexpr uint64_t da = 128 * 128 / 16 - 6, db = kPage * 128 / 16 - 6;
   if constexpr (D == 128) {
     asm volatile(
       "{\n.reg .pred e, f, t;\n.reg .b64 a, b;\n.reg .b32 lo;\n.reg .b16 m;\nelect.sync _|e, 0xffffffff;\n"
-      "setp.ne.b32 f, 0, 0;\nsetp.eq.b32 t, 0, 0;\nadd.u32 lo, %7, %1;\nmov.b64 a, {lo, %8};\nadd.u32 lo, %7, %2;\nmov.b64 b, {lo, %8};\n"
+      "setp.ne.b32 f, 0, 0;\nsetp.eq.b32 t, 0, 0;\nadd.u32 lo, %7, %1;\nmov.b64 a, {lo, %9};\nadd.u32 lo, %8, %2;\nmov.b64 b, {lo, %9};\n"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, f;\n"
       "add.s64 a, a, 2;\nadd.s64 b, b, 2;\n"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n"
@@ -149,13 +151,13 @@ __device__ __forceinline__ void issue_qk(uint32_t base, uint32_t s_full) {
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n"
       "add.s64 a, a, 2;\nadd.s64 b, b, 2;\n"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n"
-      "mov.b16 m, 3;\n@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%6 + %9], m;\n}\n"
-        ::"r"(d), "n"(a), "n"(b), "r"(id), "n"(da), "n"(db), "r"(s_full), "r"(base), "n"(kDescHigh), "n"(8 * (2 * T + PG))
+      "mov.b16 m, 3;\n@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%6 + %10], m;\n}\n"
+        ::"r"(d), "n"(a), "n"(b), "r"(id), "n"(da), "n"(db), "r"(s_full), "r"(q), "r"(k), "n"(kDescHigh), "n"(8 * (2 * T + PG))
         : "memory");
   } else {
     asm volatile(
       "{\n.reg .pred e, f, t;\n.reg .b64 a, b;\n.reg .b32 lo;\n.reg .b16 m;\nelect.sync _|e, 0xffffffff;\n"
-      "setp.ne.b32 f, 0, 0;\nsetp.eq.b32 t, 0, 0;\nadd.u32 lo, %7, %1;\nmov.b64 a, {lo, %8};\nadd.u32 lo, %7, %2;\nmov.b64 b, {lo, %8};\n"
+      "setp.ne.b32 f, 0, 0;\nsetp.eq.b32 t, 0, 0;\nadd.u32 lo, %7, %1;\nmov.b64 a, {lo, %9};\nadd.u32 lo, %8, %2;\nmov.b64 b, {lo, %9};\n"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, f;\n"
       "add.s64 a, a, 2;\nadd.s64 b, b, 2;\n"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n"
@@ -163,17 +165,16 @@ __device__ __forceinline__ void issue_qk(uint32_t base, uint32_t s_full) {
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n"
       "add.s64 a, a, 2;\nadd.s64 b, b, 2;\n"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, t;\n"
-      "mov.b16 m, 3;\n@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%6 + %9], m;\n}\n"
-        ::"r"(d), "n"(a), "n"(b), "r"(id), "n"(da), "n"(db), "r"(s_full), "r"(base), "n"(kDescHigh), "n"(8 * (2 * T + PG))
+      "mov.b16 m, 3;\n@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%6 + %10], m;\n}\n"
+        ::"r"(d), "n"(a), "n"(b), "r"(id), "n"(da), "n"(db), "r"(s_full), "r"(q), "r"(k), "n"(kDescHigh), "n"(8 * (2 * T + PG))
         : "memory");
   }
 }
-// O of tile T += P V of page PG of stage S
-template <int D, int T, int PG, int S>
-__device__ __forceinline__ void issue_pv(uint32_t base, uint32_t o_full, bool acc) {
-  using L_ = PromptSmem<D>;
+// O of tile T += P V of page PG.  v: of the stage
+template <int D, int T, int PG>
+__device__ __forceinline__ void issue_pv(uint32_t v, uint32_t o_full, bool acc) {
   constexpr uint32_t d = kColO + 128 * T, a = kColS + 128 * T + kPage * PG, id = idesc_f16(256, D);
-  constexpr uint32_t b = desc_low(L_::kV + S * L_::kVTile + PG * ((D / 2) * 128));
+  constexpr uint32_t b = desc_low(PG * ((D / 2) * 128));
   asm volatile(
       "{\n.reg .pred e, f, t;\n.reg .b64 b;\n.reg .b32 a, lo;\n.reg .b16 m;\nelect.sync _|e, 0xffffffff;\n"
       "setp.ne.b32 f, %4, 0;\nsetp.eq.b32 t, 0, 0;\nmov.b32 a, %1;\nadd.u32 lo, %6, %2;\nmov.b64 b, {lo, %7};\n"
@@ -185,18 +186,9 @@ __device__ __forceinline__ void issue_pv(uint32_t base, uint32_t o_full, bool ac
       "add.s32 a, a, 8;\nadd.s64 b, b, 2;\n"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %3, t;\n"
       "mov.b16 m, 3;\n@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5 + %8], m;\n}\n"
-      ::"r"(d), "r"(a), "n"(b), "r"(id), "r"(acc ? 1 : 0), "r"(o_full), "r"(base), "n"(kDescHigh), "n"(8 * (2 * T + PG))
+      ::"r"(d), "r"(a), "n"(b), "r"(id), "r"(acc ? 1 : 0), "r"(o_full), "r"(v), "n"(kDescHigh), "n"(8 * (2 * T + PG))
       : "memory");
 }
-// f with stage s as a constant
-template <typename F>
-__device__ __forceinline__ void by_stage(int s, F&& f) {
-  if (s == 0) f(std::integral_constant<int, 0>{});
-  else if (s == 1) f(std::integral_constant<int, 1>{});
-  else if (s == 2) f(std::integral_constant<int, 2>{});
-  else f(std::integral_constant<int, 3>{});
-}
-
 __device__ __forceinline__ void tmem_alloc2(uint32_t* dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols) : "memory");
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -223,8 +215,10 @@ __device__ __forceinline__ void arrive_smem(uint32_t bar) {
       "@e mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar)
       : "memory");
 }
-// One lane passes on to a barrier of the first CTA what its warp has acquired from a barrier of its own.
-__device__ __forceinline__ void arrive_onward(uint32_t bar) {
+// The same from the second CTA on a barrier of the first: also of what the warp
+// has acquired from a barrier of its own CTA.
+__device__ __forceinline__ void arrive_first(uint32_t bar) {
+  __syncwarp();
   asm volatile(
       "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
       "@e mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n}\n" ::"r"(bar)
@@ -272,7 +266,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
   using L_ = PromptSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  // the first CTA's: arrivals of its own warps and, from the other CTA, of the warp that passes them on
+  // the first CTA's: arrivals of its own warps and of the other CTA's, for K and V of the warp there that passes them on
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L_::kBars);  // [2] tiles, per segment
   uint64_t* kv_full = q_full + 2;                                   // [kStages]
   uint64_t* p_full = kv_full + kStages;  // [2 tiles][2 pages]; of the warps of both
@@ -283,8 +277,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
   uint64_t* o_full = s_full + 4;         // [2 tiles][2 pages]
   uint64_t* drain = o_full + 4;
   // the second CTA's: arrivals of its own warps
-  uint64_t* q_mine = drain + 1;
-  uint64_t* kv_mine = q_mine + 2;
+  uint64_t* kv_mine = drain + 1;
   // each CTA's own: seen[k % kSeen] is written
   uint64_t* seen_full = kv_mine + kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L_::kMisc);
@@ -299,16 +292,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
   const uint32_t first_bars = cluster_map(smem_u32(q_full), 0);  // the first CTA's barriers, in the order above
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + i, 5);  // four warps and the one that passes on
-      mbar_init(q_mine + i, 4);
+      mbar_init(q_full + i, 8);  // one arrival per warp, four in each CTA
       for (int h = 0; h < 2; ++h) {
-        mbar_init(p_full + 2 * i + h, 8);  // one arrival per warp, four in each CTA
+        mbar_init(p_full + 2 * i + h, 8);
         mbar_init(s_full + 2 * i + h, 1);
         mbar_init(o_full + 2 * i + h, 1);
       }
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(kv_full + i, 5);
+      mbar_init(kv_full + i, 5);  // four warps and the one that passes on
       mbar_init(kv_mine + i, 4);
       mbar_init(k_empty + i, 1);
       mbar_init(v_empty + i, 1);
@@ -389,7 +381,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
         *reinterpret_cast<uint4*>(qs + (i >> 3) * (128 * 128) + swz(row, i & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
       }
       fence_proxy_async_smem();
-      arrive_smem(smem_u32((rank == 0 ? q_full : q_mine) + t));
+      if (rank == 0) arrive_smem(smem_u32(q_full + t));
+      else arrive_first(first_bars + 8 * t);
       return pow2i(e - 140);
     };
     float down = 1.0f;
@@ -448,25 +441,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
       const int at_lo = __reduce_min_sync(0xFFFFFFFFu, at), at_hi = __reduce_max_sync(0xFFFFFFFFu, at);
       float m = -INFINITY, l = 0.0f;
       uint32_t pages = 3u;  // of the block at hand: bit i, page i counts
-      // (Before its scores come, where that costs nothing, but for the first block:
-      // a tile that had no rows in the segments before may be here while the
-      // operands are many blocks behind, and the barrier's phase an older one.
-      // Within a segment it is this block's, for the one before has been done.)
-      auto ask = [&]() {
-        ok = mbar_wait(seen_full + ks % kSeen, ks / kSeen & 1, abort_flag, p.g.status, 83);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (ok) pages = seen[ks % kSeen];
-        return ok;
-      };
       // page by page: while this warpgroup works on one page's scores, the tensor
       // core takes the other's P and refills its S
       for (int i = 0; i < 2 * nblk; ++i) {
         const int pg = i & 1;
-        if (pg == 0 && i > 0 && !ask()) break;
         ok = mbar_wait(s_full + 2 * t + pg, kc & 1, abort_flag, p.g.status, 72);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        if (i == 0 && !ask()) break;
+        if (pg == 0) {  // (by now the barrier's phase is this block's, whichever segments the tile had no rows in)
+          ok = mbar_wait(seen_full + ks % kSeen, ks / kSeen & 1, abort_flag, p.g.status, 83);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          pages = seen[ks % kSeen];
+        }
         tc_fence_after();
         const uint32_t tp = ts + kPage * pg;
         const int slot0 = (x.first + (u + (i >> 1) - x.begin)) * kBlockKeys + kPage * pg;
@@ -792,7 +779,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
         int k = 0, nk[2] = {0, 0}, ns[2] = {0, 0};  // blocks of the pair; blocks and segments of each tile
         bool ok = true;
         const uint32_t bKEmpty = smem_u32(k_empty), bVEmpty = smem_u32(v_empty), bS = smem_u32(s_full), bO = smem_u32(o_full);
-        const uint32_t base = (smem_u32(smem) & 0x3FFFFu) >> 4;
+        const uint32_t base = (smem_u32(smem) & 0x3FFFFu) >> 4, q = base + L_::kQ / 16;
+        auto k_at = [&](int s) { return base + (L_::kK + s * L_::kKTile) / 16; };
+        auto v_at = [&](int s) { return base + (L_::kV + s * L_::kVTile) / 16; };
         auto wait_for = [&](auto smem_too, uint64_t* bar, int phase, unsigned site) {
           ok = ok && bounded_wait([&]() { return pair_try_wait<smem_too.value>(bar, phase & 1); }, abort_flag, p.g.status, site);
           ok = __all_sync(0xFFFFFFFFu, ok);
@@ -808,44 +797,45 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
           wait(q_full, ns[0]++, 78);
           if (two) wait(q_full + 1, ns[1]++, 78);
           if (!ok) break;
-          by_stage(k % kStages, [&](auto s) {
-            issue_qk<D, 0, 0, s.value>(base, bS);
-            if (two) issue_qk<D, 1, 0, s.value>(base, bS);
-            issue_qk<D, 0, 1, s.value>(base, bS);
-            if (two) issue_qk<D, 1, 1, s.value>(base, bS);
-            tc_commit2(bKEmpty + 8 * s.value);
-          });
+          {
+            const int S = k % kStages;
+            const uint32_t K = k_at(S);
+            issue_qk<D, 0, 0>(q, K, bS);
+            if (two) issue_qk<D, 1, 0>(q, K, bS);
+            issue_qk<D, 0, 1>(q, K, bS);
+            if (two) issue_qk<D, 1, 1>(q, K, bS);
+            tc_commit2(bKEmpty + 8 * S);
+          }
           for (int j = 0; j < nblk && ok; ++j, ++k, ++nk[0], nk[1] += two) {
             const bool more = j + 1 < nblk;
-            if (more) wait(kv_full + (k + 1) % kStages, (k + 1) / kStages, 80);
+            const int S = k % kStages, S1 = (k + 1) % kStages;
+            if (more) wait(kv_full + S1, (k + 1) / kStages, 80);
             if (!ok) break;
-            by_stage(k % kStages, [&](auto s) {
-              constexpr int S = s.value, S1 = (S + 1) % kStages;
-              // page 0 of the tiles, then page 1: P in, the page's S of the next block out
-              wait_p(p_full, nk[0]);
-              if (!ok) return;
-              issue_pv<D, 0, 0, S>(base, bO, j > 0);
-              if (more) issue_qk<D, 0, 0, S1>(base, bS);
-              if (two) {
-                wait_p(p_full + 2, nk[1]);
-                if (!ok) return;
-                issue_pv<D, 1, 0, S>(base, bO, j > 0);
-                if (more) issue_qk<D, 1, 0, S1>(base, bS);
-              }
-              wait_p(p_full + 1, nk[0]);
-              if (!ok) return;
-              issue_pv<D, 0, 1, S>(base, bO, true);
-              if (!two) tc_commit2(bVEmpty + 8 * S);
-              if (more) issue_qk<D, 0, 1, S1>(base, bS);
-              if (two) {
-                wait_p(p_full + 3, nk[1]);
-                if (!ok) return;
-                issue_pv<D, 1, 1, S>(base, bO, true);
-                tc_commit2(bVEmpty + 8 * S);
-                if (more) issue_qk<D, 1, 1, S1>(base, bS);
-              }
-              if (more) tc_commit2(bKEmpty + 8 * S1);
-            });
+            const uint32_t V = v_at(S), K = k_at(S1);
+            // page 0 of the tiles, then page 1: P in, the page's S of the next block out
+            wait_p(p_full, nk[0]);
+            if (!ok) break;
+            issue_pv<D, 0, 0>(V, bO, j > 0);
+            if (more) issue_qk<D, 0, 0>(q, K, bS);
+            if (two) {
+              wait_p(p_full + 2, nk[1]);
+              if (!ok) break;
+              issue_pv<D, 1, 0>(V, bO, j > 0);
+              if (more) issue_qk<D, 1, 0>(q, K, bS);
+            }
+            wait_p(p_full + 1, nk[0]);
+            if (!ok) break;
+            issue_pv<D, 0, 1>(V, bO, true);
+            if (!two) tc_commit2(bVEmpty + 8 * S);
+            if (more) issue_qk<D, 0, 1>(q, K, bS);
+            if (two) {
+              wait_p(p_full + 3, nk[1]);
+              if (!ok) break;
+              issue_pv<D, 1, 1>(V, bO, true);
+              tc_commit2(bVEmpty + 8 * S);
+              if (more) issue_qk<D, 1, 1>(q, K, bS);
+            }
+            if (more) tc_commit2(bKEmpty + 8 * S1);
           }
           u = seg_end;
         }
@@ -853,21 +843,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const KvAt
       }
     } else if (rank == 1) {
       // ------------------------------------------------------ passing on
-      auto pass = [&](uint64_t* bar, int phase, uint32_t to) {
-        const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase & 1, abort_flag, p.g.status, 81));
-        if (ok) arrive_onward(to);
-        return ok;
-      };
       if (warp == kWarpMma + 1) {
-        for (int k = 0; k < end - start; ++k)
-          if (!pass(kv_mine + k % kStages, k / kStages, first_bars + 8 * (2 + k % kStages))) break;
-      } else if (warp == kWarpMma + 2) {
-        int ns[2] = {0, 0};  // in the order in which they are waited for
-        for (int u = start; u < end;) {
-          const Unit x = find_unit<kRowsPair, kBlockKeys>(p, prefix, u);
-          if (!pass(q_mine, ns[0]++, first_bars)) break;
-          if (x.r0 + 256 <= x.r1 && !pass(q_mine + 1, ns[1]++, first_bars + 8)) break;
-          u = min(end, x.end);
+        for (int k = 0; k < end - start; ++k) {
+          const int s = k % kStages;
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(kv_mine + s, k / kStages & 1, abort_flag, p.g.status, 81))) break;
+          arrive_first(first_bars + 8 * (2 + s));
         }
       }
     } else if (warp == kWarpMma + 1) {
