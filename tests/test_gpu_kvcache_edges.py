@@ -380,3 +380,27 @@ def test_prompts_from_cold_memory(fa, D, window, cap):
         # bf16 and fp16 roundings (2^-8 |O| + 2^-11 |V|), and the scores' errors (below 2^-14 here)
         assert torch.all((o.double() - ro).abs() <= 2.0 ** -8 * ro.abs() + (2.0 ** -11 + 2.0 ** -13) * 6), turn
         assert torch.all((lse.double() - rl).abs() <= 2.0 ** -14), turn
+
+
+def test_captured_calls_on_another_stream(fa):
+    """A graph whose calls run on a stream that forks off the captured one; their memory belongs to the graph."""
+    s = Setup(fa, [700, 190], [1, 1], seed=2, spare=6, columns=WIDE)
+    s.append_all()
+    q, big = (Setup._bf16(s.rng.standard_normal((n, 4, s.D))).cuda() for n in (2, 100))
+    calls = stream_calls(fa, s, q, big)
+    want = {n: f(None) for n, f in calls.items() if n != "evict"}
+    ok(fa)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = {n: calls[n](side) for n in want}
+        torch.cuda.current_stream().wait_stream(side)
+        total = sum(x.float().sum() for y in got.values() for x in y)
+    for _ in range(3):
+        for y in got.values():
+            for x in y:
+                x.fill_(3)
+        graph.replay()
+        ok(fa)
+        assert all(torch.equal(a, b) for n in want for a, b in zip(got[n], want[n])) and torch.isfinite(total)
