@@ -970,10 +970,10 @@ int tile_nt(int D, long long cols) {
 // depends on them up to 512: three tiles for D = 128, two for D = 64.  Measured
 // with 8 KV heads (us; this kernel, beyond the limits also the one for prompts):
 //   sequences x tokens  D = 128: 48 columns, 64, 80, 96     D = 64: 64 columns, 80, 96, 128
-//   1 x 8192     19  19 / 31    28 / 32    28 / 32           19   20 / 26    20 / 27    20 / 27
-//   16 x 8192   123  157 / 193  193 / 198  227 / 201         91  126 / 157  129 / 159  160 / 161
-//   64 x 4096   252  329 / 389  409 / 398  489 / 402        172  257 / 322  265 / 324  345 / 329
-//   64 x 512     92  108 / 86   150 / 86   180 / 88          65  103 / 71   106 / 72   117 / 73
+//   1 x 8192     19  19 / 30    28 / 31    28 / 31           19   20 / 26    20 / 26    20 / 27
+//   16 x 8192   122  157 / 191  193 / 195  227 / 196         90  126 / 159  129 / 159  160 / 161
+//   64 x 4096   252  329 / 390  409 / 395  489 / 402        172  257 / 322  265 / 325  345 / 328
+//   64 x 512     91  108 / 84   150 / 86   180 / 88          64  103 / 69   106 / 70   117 / 71
 // Many short sequences cross over at the limits, long ones one or two tiles
 // later; the lengths, which would tell them apart, are not known on the host.
 bool is_prompt(int D, long long cols) { return cols > (D == 128 ? 48 : 64); }

@@ -39,11 +39,11 @@
 // are written, so that its first scores are made meanwhile.
 //
 // Measured (of 1895 TFLOP/s, a large library product of bf16): D = 128, 2
-// sequences of 16384 tokens, 2048 of them new, 40 query heads over 8: 964 us,
-// 1335 TFLOP/s, 70%.  The tensor core waits 40% of the time, for the hand-offs of
-// a page's chain S -> P -> products; no unit is full (exponentials 30%, ALUs 29%,
-// issue slots 46%).  D = 64, 7 prompts of 3333 rows in all, 16 query heads over 4,
-// window 1024, capped: 72 us (without the cap 54), of which 31 remain with a
+// sequences of 16384 tokens, 2048 of them new, 40 query heads over 8: 911 us,
+// 1413 TFLOP/s, 75%.  The tensor core waits 39% of the time, for the hand-offs of
+// a page's chain S -> P -> products; no unit is full (exponentials 31%, ALUs 31%,
+// issue slots 47%).  D = 64, 7 prompts of 3333 rows in all, 16 query heads over 4,
+// window 1024, capped: 70 us (without the cap 52), of which 31 remain with a
 // window of one token: start, join, and for each of the 2
 // or 3 problems of a pair its queries, first scores and results.
 //
@@ -112,8 +112,8 @@ __device__ __forceinline__ void tc_commit2(uint32_t bar) {
 // The issuing warp shares its scheduler with two of the rows' warps, which leave
 // it one slot in three or four, so what it executes per MMA (32 to 64 cycles
 // apart) has to be little.  Descriptors are constants plus the address of shared
-// memory, added to their low word in the batch (added outside, for every stage
-// and tile, they would all be kept in registers, and spill).
+// memory, added to their low word in the batch (added outside, for every tile
+// and page, they are kept in registers, and spill).
 __host__ __device__ constexpr uint32_t desc_low(uint32_t offset) { return (offset >> 4) | (1u << 16); }
 constexpr uint32_t kDescHigh = 64u | (1u << 14) | (2u << 29);
 
@@ -121,8 +121,7 @@ constexpr uint32_t kDescHigh = 64u | (1u << 14) | (2u << 29);
 // rows N / 2 in each.  The whole warp comes here with operands that are
 // the same in every lane; one, elected once per batch, issues the MMAs of a batch
 // and the commit that reports them to both CTAs.  (Stages as template arguments
-// made four copies of the loop over the blocks, and 964 us of 928: the roles'
-// instructions share one cache.)
+// made four copies of the loop over the blocks: 964 us in place of 928.)
 // S of tile T, page PG (32 key rows of the page in each CTA).  q: of the queries'
 // tiles in shared memory, k: of the stage, addresses / 16, the same in both CTAs
 template <int D, int T, int PG>
