@@ -404,3 +404,26 @@ def test_captured_calls_on_another_stream(fa):
         graph.replay()
         ok(fa)
         assert all(torch.equal(a, b) for n in want for a, b in zip(got[n], want[n])) and torch.isfinite(total)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompts_on_two_streams_beside_other_attention(fa, D):
+    """Two prompts at once, each with memory of its own, while a third stream runs the attention of whole tensors."""
+    two = [Setup(fa, [1500, 300], [300, 280], H=4, D=D, seed=i) for i in (1, 2)]
+    for s in two:
+        s.append_all()
+    qs = [s.queries(4).cuda() for s in two]
+    x = [torch.randn((1, 4, 1024, D), device="cuda").bfloat16() for _ in range(3)]
+    want = [rows_alone(fa, s, q) for s, q in zip(two, qs)]
+    whole = fa.attention(*x)
+    ok(fa)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [[], [], []]
+    for _ in range(15):
+        for i, (s, q) in enumerate(zip(two, qs)):
+            got[i].append(rows_alone(fa, s, q, stream=streams[i]))
+        with torch.cuda.stream(streams[2]):
+            got[2].append(fa.attention(*x))
+    ok(fa)
+    for g, w in zip(got, want + [whole]):
+        assert all(torch.equal(a, b) for y in g for a, b in zip(y, w))
